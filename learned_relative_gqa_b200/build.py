@@ -17,7 +17,7 @@ LIB_NAME = "libinkling_rel_attn.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 # the same kernels with every shared / global index checked (-DINKLING_BOUNDS_CHECK), for tests
 BOUNDS_CHECK_LIB_PATH = os.path.join(HERE, "libinkling_rel_attn_boundscheck.so")
-SOURCES = ["host.cu", "prep_kernels.cu", "fwd.cu", "bwd.cu", "l2clip.cu"]
+SOURCES = ["host.cu", "prep_kernels.cu", "fwd.cu", "bwd.cu", "l2clip.cu", "paged_cache.cu", "decode.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
