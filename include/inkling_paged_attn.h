@@ -133,15 +133,16 @@ inkling_status inkling_kv_append(const inkling_kv_cache_desc* cache, const inkli
  * key has (the rest of the last page) may be anything, NaN and infinities included.
  * A request with no allowed key (lens[n] <= 0: a padding row) gets out = 0, lse =
  * sink. A length above max_pages * page_size is taken as that.
- *   requests N, heads_q Hq (a multiple of heads_kv, below 65536), rel_extent R,
- *   window W (0: all), max_pages M; scale <= 0 means head_dim^-0.5
+ *   requests N, heads_q Hq (a multiple of heads_kv, below 65536), rel_extent R (a
+ *   multiple of 8), window W (0: all), max_pages M; scale <= 0 means head_dim^-0.5
  *   q [N,Hq,D] BF16; profiles [N,Hq,R] BF16 (NULL exactly when R == 0); sink [N,Hq]
  *   FP32 or NULL (no sink); block_table [N,M] int32; lens [N] int32;
  *   out [N,Hq,D] FP32; lse [N,Hq] FP32; k_scale, v_scale as in inkling_kv_append
  * q, profiles, out, the pools and the workspace are 16-byte aligned, the rest 4.
  * The result of a request does not depend on where its pages are; it depends, in the
  * rounding of its sums alone, on the lengths in its batch. Equal calls give equal bits.
- * Limits (INKLING_ERR_UNSUPPORTED): N < 2^24, M * page_size, R and W < 2^30.
+ * Limits (INKLING_ERR_UNSUPPORTED): N < 2^24, M * page_size, R and W < 2^30,
+ * N * Hq * M * page_size < 2^40.
  */
 typedef struct {
     int64_t requests, heads_q, rel_extent, window, max_pages;

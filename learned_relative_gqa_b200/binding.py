@@ -559,6 +559,13 @@ def inkling_rel_attn_decode_workspace_size(cache: KVCacheDesc, dims: DecodeDims)
     return int(load().inkling_rel_attn_decode_workspace_size(ctypes.byref(cache), ctypes.byref(dims)))
 
 
+def alloc_decode_workspace(cache: KVCacheDesc, dims: DecodeDims, device) -> torch.Tensor:
+    n = inkling_rel_attn_decode_workspace_size(cache, dims)
+    if n == 0:
+        raise InklingError(INKLING_ERR_INVALID_ARG, "inkling_rel_attn_decode_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def inkling_rel_attn_decode(cache: KVCacheDesc, dims: DecodeDims, q, k_cache, v_cache, k_scale, v_scale, profiles,
                             sink, block_table, lens, out, lse, workspace, stream=None) -> None:
     with torch.cuda.device(k_cache.device):

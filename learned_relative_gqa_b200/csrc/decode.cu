@@ -10,25 +10,29 @@
 //
 // Every cached value is read once and used for the Hq / Hkv query heads of its group, 2 to
 // 16 products per byte: bound by HBM. So the work is laid out for bytes in flight:
-//   * the grid is two CTAs of four warps per SM, whatever the batch; all CTA tiles (4 warps
-//     x KT keys) of all (request, KV head) units are numbered through and each CTA takes an
+//   * each warp is a worker of its own, eight to an SM whatever the batch. The tiles of KT
+//     keys of all (request, KV head) units are numbered through and each worker takes an
 //     equal run of them, so ragged batches and single long requests load every SM the same.
 //     The run is found on the device from the lengths: nothing about them is needed on the
-//     host. A unit that is cut leaves its parts in the workspace and a second kernel,
-//     launched while the first one runs, joins them in the order of the keys.
-//   * each warp streams tiles of its own through a private cp.async ring in shared memory
-//     (no block barrier inside a unit) and keeps its own m, l and O; the four are joined
-//     once per unit. cp.async with one row address per key takes any page size and any
-//     strides, and fills the rows of keys that are not allowed with zeros, so nothing that
-//     stands in such a place (NaN, infinities) reaches a product.
+//     host. A unit that is cut leaves its parts in the workspace and a second kernel joins
+//     them in the order of the keys.
+//   * a worker streams its tiles through a private cp.async ring in shared memory that
+//     runs on over the ends of units (the next unit's tiles are on their way while the last
+//     one's result is written) with no block barrier anywhere in the loop. cp.async with
+//     one row address per key takes any page size and any strides, and fills the rows of
+//     keys that are not allowed with zeros, so nothing that stands in such a place (NaN,
+//     infinities) reaches a product. The profile entries of a tile's distances come through
+//     the same ring.
 //   * products are mma.sync m16n8k16: with a group of 8 heads or fewer a tile is far too
 //     narrow for tcgen05 (64 or 128 rows of M), and the tensor pipe is idle most of the
 //     time anyway. S[heads, keys] = Q K^T puts the heads in M, so its accumulators are
 //     already the B operand of O^T[d, heads] = V^T P^T: no shuffle between the products.
 //     K fragments come by ldmatrix, V fragments by its transposing form.
-//   * probabilities enter the second product as the sum of two 16-bit numbers (p and what
-//     its rounding left), which costs one more mma on an idle pipe and keeps the FP32
-//     result to about 2^-18 of a probability instead of 2^-9.
+//   * probabilities enter the second product as a sum of 16-bit numbers (p, what its
+//     rounding left, and for BF16 what that one's left), which costs one or two more mma on
+//     an idle pipe and keeps the FP32 result to 2^-22 of a probability or less, where one
+//     number would keep 2^-9. Each tile's product starts from zero and is added to O in
+//     FP32, as the tensor pipe's own sum is cut off, not rounded, and would drift.
 // e4m3 caches: a code is exact in FP16, so both products run in FP16 with FP32 sums; the
 // scales stay outside the products. q (BF16) is first multiplied by a power of two per
 // head that brings its largest value into [1, 2): exact but for values below 2^-14 of
@@ -51,15 +55,18 @@ using namespace ira;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCtasPerSm = 2;
-constexpr int kMaxCtas = 320;  // workspace slots: two per CTA
-constexpr int kMaxHeads = 16;  // query heads of a unit at most
+constexpr int kMaxCtas = 320;
+constexpr int kMaxWorkers = kMaxCtas * kWarps;  // workspace slots: two per worker
+constexpr int kMinTiles = 2;                    // tiles that a worker takes at least, where there are enough
+constexpr int kJoinThreads = 1024;
 
-struct Rec {  // what a CTA's last unit left unfinished: parts 1 .. more are in the next CTAs
-    int n, u, more, pad;
+struct Rec {  // a worker's last unit, if it began there and did not end: its other parts are
+    int n, u, more, pad;  // the first ones of the next `more` workers
 };
 
 struct DecodeParams {
-    int N, Hq, Hkv, group, hblocks, R, W, M, P, num_pages, cap;
+    int N, Hq, Hkv, group, hblocks, unit_heads, R, W, M, P, num_pages, cap;
+    uint32_t p_mul, p_shift;  // j / P = j p_mul >> p_shift
     int64_t page_stride, token_stride, head_stride;  // bytes
     float scale_log2;
     const uint16_t* q;
@@ -73,9 +80,9 @@ struct DecodeParams {
     const int32_t* lens;
     float* out;
     float* lse;
-    Rec* rec;          // [grid]
-    float2* part_ml;   // [2 * grid][kMaxHeads]
-    float* part_o;     // [2 * grid][kMaxHeads][D]
+    Rec* rec;          // [workers of the grid]
+    float2* part_ml;   // [2 * workers][unit_heads]
+    float* part_o;     // [2 * workers][unit_heads][D]
 };
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -128,36 +135,39 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
 }
 
 // Shape of one instantiation. D head_dim, NT groups of 8 query heads (1 or 2), F8 e4m3
-// cache. A tile is 8 KB of K and V in every form but the smallest, so that three of them
-// per warp are 64 KB or more in flight on an SM.
+// cache. A tile is 8 KB of K and V in every form but the smallest, so that the two or three
+// of each worker that are on their way are 128 KB or more on an SM.
 template <int D_, int NT_, bool F8_>
 struct Shape {
     static constexpr int D = D_, NT = NT_;
     static constexpr bool F8 = F8_;
     static constexpr int ES = F8 ? 1 : 2;
-    static constexpr int RB = D * ES;                    // bytes of a row
-    static constexpr int CPR = RB / 16;                  // 16-byte chunks of a row
-    static constexpr int KT = (D == 128 && !F8) ? 16 : 32;  // keys of a warp's tile
-    static constexpr int CT = kWarps * KT;               // keys of a CTA tile
+    static constexpr int RB = D * ES;                       // bytes of a row
+    static constexpr int CPR = RB / 16;                     // 16-byte chunks of a row
+    static constexpr int KT = (D == 128 && !F8) ? 16 : 32;  // keys of a tile
     static constexpr int STAGES = 3;
-    static constexpr int SIDE = KT * RB;                 // bytes of K (or V) in a stage
-    static constexpr int RING = STAGES * 2 * SIDE;       // bytes of a warp's ring
-    static constexpr int OROW = D + 4;                   // floats of a head's row in the join (no bank conflicts)
-    static constexpr int REGION = RING > 8 * NT * OROW * 4 ? RING : 8 * NT * OROW * 4;  // the join reuses the ring
-    static constexpr int SMEM = kWarps * REGION;
+    static constexpr int SIDE = KT * RB;                    // bytes of K (or V) in a stage
+    static constexpr int BCH = KT / 8 + 1;                  // 16-byte chunks that hold KT profile entries
+    static constexpr int STAGE = 2 * SIDE + 8 * NT * BCH * 16;
+    static constexpr int SMEM = kWarps * STAGES * STAGE;
+    // chunk c of row r stands at chunk c ^ swz(r): ldmatrix's eight rows use all banks
     __device__ static __forceinline__ int swz(int row) { return RB >= 128 ? (row & 7) : ((row >> 1) & 3); }
 };
 
-struct Span {  // allowed keys [lo, len) of a request and its CTA tiles (at least one)
+struct Span {  // allowed keys [lo, len) of a request and its tiles (at least one)
     int lo, len, tiles;
 };
-template <int CT>
-__device__ __forceinline__ Span span_of(const DecodeParams& p, int n) {
+template <int KT>
+__device__ __forceinline__ Span span_of(const DecodeParams& p, int raw_len) {
     Span s;
-    s.len = min(max(p.lens[n], 0), p.cap);
+    s.len = min(max(raw_len, 0), p.cap);
     s.lo = p.W > 0 ? max(s.len - p.W, 0) : 0;
-    s.tiles = max((s.len - s.lo + CT - 1) / CT, 1);
+    s.tiles = max((s.len - s.lo + KT - 1) / KT, 1);
     return s;
+}
+
+__device__ __forceinline__ int page_index(const DecodeParams& p, int j) {
+    return int((uint64_t(uint32_t(j)) * p.p_mul) >> p.p_shift);
 }
 
 // lse of a row from the maximum of its keys' logits, that of those and the sink (log2 units),
@@ -167,29 +177,40 @@ __device__ __forceinline__ float lse_of(float keys, float top, float total, cons
     return (top + log2f(total)) * kLn2;
 }
 
+// exp2(x - top), 1 where both are the same infinity
+__device__ __forceinline__ float weight(float x, float top) { return x == top ? 1.f : ex2_approx(x - top); }
+
+enum : int { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8 };  // of a run of tiles of one unit
+
+// Position in the numbered tiles: request, unit of it, tile of that.
+struct Cursor {
+    Span s;
+    int n, u, t, next_len;
+};
+
 template <class S>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __grid_constant__ DecodeParams p) {
     constexpr int D = S::D, NT = S::NT, KT = S::KT, ST = S::STAGES;
     constexpr bool F8 = S::F8;
     constexpr int NS = KT / 8;  // S accumulator tiles of 8 keys
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint32_t s_mask[kWarps][ST];
-    __shared__ float2 s_ml[kWarps][8 * NT];
+    __shared__ int4 s_tile[kWarps][ST];    // request, unit, first key, length
+    __shared__ uint2 s_flags[kWarps][ST];  // allowed keys of the tile, kFirst ..
     __shared__ long long s_sum[kWarps];
-    __shared__ long long s_base;
-    __shared__ int s_n;
+    __shared__ long long s_base[kWarps];
+    __shared__ int s_n[kWarps];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     // the joining kernel may be set up now; it waits for this one's results itself
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // ---- this CTA's run of tiles
-    const int64_t units = int64_t(p.Hkv) * p.hblocks;  // per request
+    // ---- this worker's run of tiles
+    const int units = p.Hkv * p.hblocks;  // per request
     const int chunk = (p.N + kThreads - 1) / kThreads;
     const int n0 = min(tid * chunk, p.N), n1 = min(n0 + chunk, p.N);
     long long own = 0;
-    for (int n = n0; n < n1; ++n) own += span_of<S::CT>(p, n).tiles;
+    for (int n = n0; n < n1; ++n) own += span_of<KT>(p, p.lens[n]).tiles;
     long long inc = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -205,189 +226,210 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
         all += s_sum[w];
     }
     all *= units;
-    const int ctas = int(all < gridDim.x ? all : (long long)gridDim.x);
-    const int cta = blockIdx.x;
-    if (cta >= ctas) {
-        if (tid == 0) p.rec[cta] = Rec{0, 0, 0, 0};
-        return;
-    }
-    const long long first = cta * all / ctas, last = (cta + 1) * all / ctas;
-    if (before * units <= first && first < (before + own) * units) {
-        long long at = before * units;
-        int n = n0;
-        for (;; ++n) {
-            const long long size = span_of<S::CT>(p, n).tiles * units;
-            if (first < at + size) break;
-            at += size;
+    before *= units;
+    const long long enough = (all + kMinTiles - 1) / kMinTiles;
+    const int workers = int(enough < (long long)gridDim.x * kWarps ? enough : (long long)gridDim.x * kWarps);
+    // neighbours in the order of the tiles are on different SMs
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const long long first = (long long)(w * gridDim.x + blockIdx.x) * all / workers;
+        if (before <= first && first < before + own * units) {
+            long long at = before;
+            int n = n0;
+            for (;; ++n) {
+                const long long size = (long long)span_of<KT>(p, p.lens[n]).tiles * units;
+                if (first < at + size) break;
+                at += size;
+            }
+            s_n[w] = n;
+            s_base[w] = at;
         }
-        s_n = n;
-        s_base = at;
     }
     __syncthreads();
-    int n = s_n;
-    long long base = s_base;
+    const int worker = warp * gridDim.x + blockIdx.x;
+    if (worker >= workers) {
+        if (lane == 0) p.rec[worker] = Rec{0, 0, 0, 0};
+        return;
+    }
+    const long long first = worker * all / workers;
+    const int total = int((worker + 1) * all / workers - first);
 
-    const uint32_t ring = smem_u32(smem) + warp * S::REGION;
-    const float* const ofloat = reinterpret_cast<const float*>(smem);
+    const uint32_t ring = smem_u32(smem) + warp * ST * S::STAGE;
+
+    // ---- producer: lane r < KT looks key r of a tile up, all lanes copy
+    const int my_key = lane & (KT - 1);
+    auto advance = [&](Cursor& c) {
+        if (++c.t < c.s.tiles) return;
+        c.t = 0;
+        if (++c.u < units) return;
+        c.u = 0;
+        ++c.n;
+        c.s = span_of<KT>(p, c.next_len);
+        c.next_len = c.n + 1 < p.N ? p.lens[c.n + 1] : 0;
+    };
+    auto lookup = [&](const Cursor& c) {  // -1: not allowed
+        const int j = c.s.lo + c.t * KT + my_key;
+        return j < c.s.len ? p.table[int64_t(c.n) * p.M + page_index(p, j)] : -1;
+    };
+    auto issue = [&](const Cursor& c, int i, int stage, int page) {
+        const int j0 = c.s.lo + c.t * KT, j = j0 + my_key;
+        const int kvh = c.u / p.hblocks, hb = c.u - kvh * p.hblocks;
+        const int head0 = kvh * p.group + hb * 8 * NT;
+        const bool ok = page >= 0 && page < p.num_pages;
+        const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+        const bool run = i == 0 || c.t == 0;
+        if (lane == 0) {
+            s_tile[warp][stage] = make_int4(c.n, c.u, j0, c.s.len);
+            s_flags[warp][stage] =
+                make_uint2(mask, (run ? kFirst : 0) | (i == total - 1 || c.t == c.s.tiles - 1 ? kLast : 0) |
+                                     (c.t == 0 ? kBegins : 0) | (c.t == c.s.tiles - 1 ? kEnds : 0));
+        }
+        const int64_t at = ok ? int64_t(page) * p.page_stride +
+                                    int64_t(j - page_index(p, j) * p.P) * p.token_stride + kvh * p.head_stride
+                              : 0;
+        const uint32_t dst = ring + stage * S::STAGE;
+#pragma unroll
+        for (int x = 0; x < KT * S::CPR / 32; ++x) {
+            const int r = x * (32 / S::CPR) + lane / S::CPR, ch = lane % S::CPR;
+            const int64_t off = __shfl_sync(0xffffffffu, at, r) + ch * 16;
+            const uint32_t bytes = (mask >> r) & 1u ? 16u : 0u;
+            const uint32_t to = dst + r * S::RB + ((ch ^ S::swz(r)) << 4);
+            cp_async_16(to, p.k_cache + off, bytes);
+            cp_async_16(to + S::SIDE, p.v_cache + off, bytes);
+        }
+        // profile entries of the distances [dlo, dlo + KT), in whole chunks of 8
+        const int dlo = c.s.len - KT - j0;
+        const int heads = min(8 * NT, p.group - hb * 8 * NT);
+        if (p.R > 0 && dlo < p.R) {
+            const int c0 = dlo >> 3;
+#pragma unroll
+            for (int x = lane; x < 8 * NT * S::BCH; x += 32) {
+                const int h = x / S::BCH, ch = c0 + x - h * S::BCH;
+                const bool in = h < heads && ch >= 0 && ch < (p.R >> 3);
+                const int64_t off = in ? (int64_t(c.n) * p.Hq + head0 + h) * p.R + ch * 8 : 0;
+                cp_async_16(dst + 2 * S::SIDE + x * 16, p.profiles + off, in ? 16u : 0u);
+            }
+        }
+        if (run) {  // q and the sink are loaded when the tile's turn comes: warm L2 for that
+            if (lane < heads * D / 64) prefetch_l2(p.q + (int64_t(c.n) * p.Hq + head0) * D + lane * 64);
+            if (lane == 31 && p.sink) prefetch_l2(p.sink + int64_t(c.n) * p.Hq + head0);
+        }
+    };
+
+    Cursor cur;
+    int page = -1, made = 0;
+    {
+        cur.n = s_n[warp];
+        cur.s = span_of<KT>(p, p.lens[cur.n]);
+        cur.next_len = cur.n + 1 < p.N ? p.lens[cur.n + 1] : 0;
+        const long long local = first - s_base[warp];
+        cur.u = int(local / cur.s.tiles);
+        cur.t = int(local - (long long)cur.u * cur.s.tiles);
+        // the first lookups go out together
+        Cursor at[ST];
+        int pages[ST];
+#pragma unroll
+        for (int i = 0; i < ST; ++i) {
+            at[i] = cur;
+            pages[i] = -1;
+            if (i < total) {
+                if (i > 0) {
+                    at[i] = at[i - 1];
+                    advance(at[i]);
+                }
+                pages[i] = lookup(at[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) {
+            if (i < total) issue(at[i], i, i, pages[i]);
+            cp_async_commit();
+        }
+        made = min(ST - 1, total);
+        cur = at[ST - 1];
+        page = pages[ST - 1];
+    }
+
+    uint32_t qa[D / 16][2 * NT];
+    float zscale[NT], sink[NT];
+    float o[D / 16][NT][4];
+    float mx[NT], sum[NT];
+    int head0 = 0, heads = 0;
+    bool begins = false;
     Rec rec{0, 0, 0, 0};
 
-    for (long long pos = first; pos < last;) {
-        const Span sp = span_of<S::CT>(p, n);
-        const long long local = pos - base;
-        const int u = int(local / sp.tiles), tile0 = int(local - (long long)u * sp.tiles);
-        const long long room = last - pos;
-        const int tile1 = int(sp.tiles - tile0 < room ? sp.tiles : tile0 + room);
-        const int kvh = u / p.hblocks, hb = u - kvh * p.hblocks;
-        const int head0 = kvh * p.group + hb * 8 * NT;
-        const int heads = min(8 * NT, p.group - hb * 8 * NT);
-        const int nt = tile1 - tile0;  // tiles of each warp
-        const int key_end = min((long long)sp.len, sp.lo + (long long)tile1 * S::CT);
-        const int key0 = sp.lo + tile0 * S::CT + warp * KT;  // first key of this warp's tile 0; step CT
-        const int32_t* const row = p.table + int64_t(n) * p.M;
-
-        // ---- q fragments
-        uint32_t qa[D / 16][2 * NT];
-        float zscale[NT];
-#pragma unroll
-        for (int r = 0; r < NT; ++r) {
-            const int h = g + 8 * r;
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (int64_t(n) * p.Hq + head0 + h) * D);
-            zscale[r] = p.scale_log2;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                // BF16: columns 16 ks + {2t, 2t+1} and + 8; e4m3: 16 ks + {4t .. 4t+3}, the
-                // order in which a code word holds them (K uses the same one)
-                const int w0 = F8 ? 8 * ks + 2 * t : 8 * ks + t, w1 = F8 ? w0 + 1 : w0 + 4;
-                qa[ks][2 * r] = h < heads ? src[w0] : 0u;
-                qa[ks][2 * r + 1] = h < heads ? src[w1] : 0u;
-            }
-            if constexpr (F8) {
-                float top = 0.f;
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 x = unpack2<false>(qa[ks][2 * r + i]);
-                        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
-                    }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // 2^e <= top < 2^(e+1) (zero, subnormal and infinite rows: the nearest normal power)
-                const int e = min(max(int(__float_as_uint(top) >> 23) - 127, -126), 126);
-                const float down = __uint_as_float(uint32_t(127 - e) << 23);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 x = unpack2<false>(qa[ks][2 * r + i]);
-                        qa[ks][2 * r + i] = pack2<true>(x.x * down, x.y * down);
-                    }
-                zscale[r] *= __uint_as_float(uint32_t(127 + e) << 23) * p.k_scale[kvh];
+    int stage = 0;
+    for (int i = 0; i < total; ++i) {
+        cp_async_wait_group<ST - 2>();
+        __syncwarp();  // the tile is in, and every lane is done with the previous one's stage
+        if (made < total) {
+            issue(cur, made, stage == 0 ? ST - 1 : stage - 1, page);
+            if (++made < total) {
+                advance(cur);
+                page = lookup(cur);
             }
         }
+        cp_async_commit();
 
-        float o[D / 16][NT][4];
-#pragma unroll
-        for (int m = 0; m < D / 16; ++m)
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[m][x][i] = 0.f;
-        float mx[NT], sum[NT];
-#pragma unroll
-        for (int r = 0; r < NT; ++r) {
-            mx[r] = -INFINITY;
-            sum[r] = 0.f;
-        }
+        const int4 tile = s_tile[warp][stage];
+        const uint32_t mask = s_flags[warp][stage].x, flags = s_flags[warp][stage].y;
+        const int n = tile.x, u = tile.y;
+        const uint32_t kbase = ring + stage * S::STAGE, vbase = kbase + S::SIDE, bbase = vbase + S::SIDE;
+        stage = stage == ST - 1 ? 0 : stage + 1;
 
-        // ---- producer: lane r < KT looks key r of a tile up, all lanes copy
-        const int my_key = lane & (KT - 1);
-        auto page_of = [&](int i) {  // -1: not allowed
-            const int j = key0 + i * S::CT + my_key;
-            return i < nt && j < key_end ? row[j / p.P] : -1;
-        };
-        auto issue = [&](int i, int stage, int page) {
-            const int j = key0 + i * S::CT + my_key;
-            const bool ok = page >= 0 && page < p.num_pages;
-            const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-            if (lane == 0) s_mask[warp][stage] = mask;
-            const int64_t at =
-                ok ? int64_t(page) * p.page_stride + int64_t(j % p.P) * p.token_stride + kvh * p.head_stride : 0;
-            const uint32_t dst = ring + stage * 2 * S::SIDE;
-#pragma unroll
-            for (int c = 0; c < KT * S::CPR / 32; ++c) {
-                const int r = c * (32 / S::CPR) + lane / S::CPR, ch = lane % S::CPR;
-                const int64_t off = __shfl_sync(0xffffffffu, at, r) + ch * 16;
-                const uint32_t bytes = (mask >> r) & 1u ? 16u : 0u;
-                const uint32_t to = dst + r * S::RB + ((ch ^ S::swz(r)) << 4);
-                cp_async_16(to, p.k_cache + off, bytes);
-                cp_async_16(to + S::SIDE, p.v_cache + off, bytes);
-            }
-        };
-        // ---- bias of this thread's S entries of tile i (BF16 bits, 0 beyond the profile)
-        const bool biased = p.R > 0;
-        uint16_t bias[NT][NS][2];
-        auto load_bias = [&](int i) {
-            const int j0 = key0 + i * S::CT;
-#pragma unroll
-            for (int r = 0; r < NT; ++r)
-#pragma unroll
-                for (int s = 0; s < NS; ++s) bias[r][s][0] = bias[r][s][1] = 0;
-            if (!biased || i >= nt || sp.len - 1 - (j0 + KT - 1) >= p.R) return;
+        if (flags & kFirst) {
+            begins = flags & kBegins;
+            const int kvh = u / p.hblocks, hb = u - kvh * p.hblocks;
+            head0 = kvh * p.group + hb * 8 * NT;
+            heads = min(8 * NT, p.group - hb * 8 * NT);
 #pragma unroll
             for (int r = 0; r < NT; ++r) {
-                if (g + 8 * r >= heads) continue;
-                const uint16_t* prof = p.profiles + (int64_t(n) * p.Hq + head0 + g + 8 * r) * p.R;
+                const int h = g + 8 * r;
+                const int64_t at = int64_t(n) * p.Hq + head0 + h;
+                const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + at * D);
+                zscale[r] = p.scale_log2;
+                sink[r] = p.sink && h < heads ? p.sink[at] * kLog2e : -INFINITY;
+                mx[r] = -INFINITY;
+                sum[r] = 0.f;
 #pragma unroll
-                for (int s = 0; s < NS; ++s)
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    // BF16: columns 16 ks + {2t, 2t+1} and + 8; e4m3: 16 ks + {4t .. 4t+3}, the
+                    // order in which a code word holds them (K uses the same one)
+                    const int w0 = F8 ? 8 * ks + 2 * t : 8 * ks + t, w1 = F8 ? w0 + 1 : w0 + 4;
+                    qa[ks][2 * r] = h < heads ? src[w0] : 0u;
+                    qa[ks][2 * r + 1] = h < heads ? src[w1] : 0u;
+                }
+                if constexpr (F8) {
+                    float top = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int d = sp.len - 1 - (j0 + 8 * s + 2 * t + e);
-                        if (d >= 0 && d < p.R) bias[r][s][e] = __ldg(prof + d);
-                    }
-            }
-        };
-
-        int page = -1;
-        {
-            int first_pages[ST - 1];
+                    for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-            for (int i = 0; i < ST - 1; ++i) first_pages[i] = page_of(i);
-            page = page_of(ST - 1);
+                        for (int e = 0; e < 2; ++e) {
+                            const float2 x = unpack2<false>(qa[ks][2 * r + e]);
+                            top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+                        }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // 2^e <= top < 2^(e+1) (zero, subnormal and infinite rows: the nearest normal power)
+                    const int e = min(max(int(__float_as_uint(top) >> 23) - 127, -126), 126);
+                    const float down = __uint_as_float(uint32_t(127 - e) << 23);
 #pragma unroll
-            for (int i = 0; i < ST - 1; ++i) {
-                if (i < nt) issue(i, i, first_pages[i]);
-                cp_async_commit();
+                    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float2 x = unpack2<false>(qa[ks][2 * r + y]);
+                            qa[ks][2 * r + y] = pack2<true>(x.x * down, x.y * down);
+                        }
+                    zscale[r] *= __uint_as_float(uint32_t(127 + e) << 23) * p.k_scale[kvh];
+                }
+#pragma unroll
+                for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[m][r][e] = 0.f;
             }
         }
-        load_bias(0);
 
-        int stage = 0;
-        for (int i = 0; i < nt; ++i) {
-            cp_async_wait_group<ST - 2>();
-            __syncwarp();  // the tile is in, and every lane is done with the previous one's stage
-            {
-                const int next = i + ST - 1;
-                const int to = stage == 0 ? ST - 1 : stage - 1;
-                if (next < nt) issue(next, to, page);
-                cp_async_commit();
-                page = page_of(next + 1);
-            }
-            uint16_t b_now[NT][NS][2];
-#pragma unroll
-            for (int r = 0; r < NT; ++r)
-#pragma unroll
-                for (int s = 0; s < NS; ++s) {
-                    b_now[r][s][0] = bias[r][s][0];
-                    b_now[r][s][1] = bias[r][s][1];
-                }
-            load_bias(i + 1);
-
-            const uint32_t mask = s_mask[warp][stage];
-            const uint32_t kbase = ring + stage * 2 * S::SIDE, vbase = kbase + S::SIDE;
-            stage = stage == ST - 1 ? 0 : stage + 1;
-            if (mask == 0) continue;
-
+        if (mask != 0) {
             // lane's row and chunk parity in the 16-key ldmatrix of either side
             const int lrow = (lane & 7) + ((lane >> 4) << 3), lch = (lane >> 3) & 1;
             const int lswz = S::swz(lane & 7);
@@ -423,7 +465,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
             }
 
             // ---- logits in log2 units, their maximum, the running state
+#pragma unroll
+            for (int r = 0; r < NT; ++r)
+#pragma unroll
+                for (int x = 0; x < NS; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) s[x][2 * r + e] *= zscale[r];
+            const int dlo = tile.w - KT - tile.z;
+            if (p.R > 0 && dlo < p.R) {
+#pragma unroll
+                for (int r = 0; r < NT; ++r) {
+                    // entry of key x of the tile: the one of distance dlo + KT - 1 - x
+                    const uint32_t at = bbase + (g + 8 * r) * (S::BCH * 16) + ((dlo & 7) + KT - 1 - 2 * t) * 2;
+#pragma unroll
+                    for (int x = 0; x < NS; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            s[x][2 * r + e] = fmaf(__uint_as_float(lds_u16(at - (8 * x + e) * 2) << 16), kLog2e,
+                                                   s[x][2 * r + e]);
+                }
+            }
             float top[NT];
+            bool grows = false;
 #pragma unroll
             for (int r = 0; r < NT; ++r) {
                 top[r] = -INFINITY;
@@ -431,23 +494,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
                 for (int x = 0; x < NS; ++x)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float z = s[x][2 * r + e] * zscale[r];
-                        z = fmaf(__uint_as_float(uint32_t(b_now[r][x][e]) << 16), kLog2e, z);
-                        if (!((mask >> (8 * x + 2 * t + e)) & 1u)) z = -INFINITY;
-                        s[x][2 * r + e] = z;
-                        top[r] = fmaxf(top[r], z);
+                        if (!((mask >> (8 * x + 2 * t + e)) & 1u)) s[x][2 * r + e] = -INFINITY;
+                        top[r] = fmaxf(top[r], s[x][2 * r + e]);
                     }
                 top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
                 top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+                grows |= top[r] > mx[r] + kRescaleThreshold;
             }
-            bool grows = false;
-#pragma unroll
-            for (int r = 0; r < NT; ++r) grows |= top[r] > mx[r] + kRescaleThreshold;
             if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
                 for (int r = 0; r < NT; ++r) {
                     const float now = fmaxf(mx[r], top[r]);
-                    const float f = mx[r] == now ? 1.f : ex2_approx(mx[r] - now);
+                    const float f = weight(mx[r], now);
                     mx[r] = now;
                     sum[r] *= f;
                     // heads of this thread's O columns: 2t, 2t + 1 (+ 8 r)
@@ -461,156 +519,264 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
                     }
                 }
             }
-            uint32_t hi[NT][NS], lo[NT][NS];
+            constexpr int TERMS = F8 ? 2 : 3;  // 16-bit numbers of a probability
+            uint32_t pr[TERMS][NT][NS];
 #pragma unroll
             for (int r = 0; r < NT; ++r) {
                 const float ref = mx[r] == -INFINITY ? 0.f : mx[r];
 #pragma unroll
                 for (int x = 0; x < NS; ++x) {
-                    const float p0 = ex2_approx(s[x][2 * r] - ref), p1 = ex2_approx(s[x][2 * r + 1] - ref);
+                    float p0 = ex2_approx(s[x][2 * r] - ref), p1 = ex2_approx(s[x][2 * r + 1] - ref);
                     sum[r] += p0 + p1;
-                    hi[r][x] = pack2<F8>(p0, p1);
-                    const float2 b = unpack2<F8>(hi[r][x]);
-                    lo[r][x] = pack2<F8>(p0 - b.x, p1 - b.y);
+#pragma unroll
+                    for (int k = 0; k < TERMS; ++k) {
+                        pr[k][r][x] = pack2<F8>(p0, p1);
+                        const float2 b = unpack2<F8>(pr[k][r][x]);
+                        p0 -= b.x;
+                        p1 -= b.y;
+                    }
                 }
             }
 
             // ---- O^T += V^T P^T
 #pragma unroll
             for (int c = 0; c < S::CPR / 2; ++c) {
+                constexpr int MT = F8 ? 2 : 1;  // 16-column tiles of a pair of chunks
+                float acc[MT][NT][4];
+#pragma unroll
+                for (int x = 0; x < MT; ++x)
+#pragma unroll
+                    for (int r = 0; r < NT; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[x][r][e] = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < KT / 16; ++kk) {
                     uint32_t f[4];
                     ldmatrix_x4_trans(vbase + (kk * 16 + lrow) * S::RB + (((2 * c + lch) ^ lswz) << 4), f);
-                    if constexpr (!F8) {
 #pragma unroll
-                        for (int r = 0; r < NT; ++r) {
-                            mma16816<false>(o[c][r], f[0], f[1], f[2], f[3], hi[r][2 * kk], hi[r][2 * kk + 1]);
-                            mma16816<false>(o[c][r], f[0], f[1], f[2], f[3], lo[r][2 * kk], lo[r][2 * kk + 1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
+                    for (int x = 0; x < MT; ++x) {
+                        uint32_t a0 = f[0], a1 = f[1], a2 = f[2], a3 = f[3];
+                        if constexpr (F8) {
                             // a 16-bit unit holds columns 2g, 2g + 1 of one key: regroup by column
                             const uint32_t w0 = __byte_perm(f[x], 0, 0x3120), w1 = __byte_perm(f[x + 2], 0, 0x3120);
-                            const uint32_t a0 = e4m3x2_to_f16x2(w0), a1 = e4m3x2_to_f16x2(w0 >> 16);
-                            const uint32_t a2 = e4m3x2_to_f16x2(w1), a3 = e4m3x2_to_f16x2(w1 >> 16);
+                            a0 = e4m3x2_to_f16x2(w0);
+                            a1 = e4m3x2_to_f16x2(w0 >> 16);
+                            a2 = e4m3x2_to_f16x2(w1);
+                            a3 = e4m3x2_to_f16x2(w1 >> 16);
+                        }
 #pragma unroll
-                            for (int r = 0; r < NT; ++r) {
-                                mma16816<true>(o[2 * c + x][r], a0, a1, a2, a3, hi[r][2 * kk], hi[r][2 * kk + 1]);
-                                mma16816<true>(o[2 * c + x][r], a0, a1, a2, a3, lo[r][2 * kk], lo[r][2 * kk + 1]);
-                            }
+                        for (int r = 0; r < NT; ++r)
+#pragma unroll
+                            for (int k = TERMS - 1; k >= 0; --k)
+                                mma16816<F8>(acc[x][r], a0, a1, a2, a3, pr[k][r][2 * kk], pr[k][r][2 * kk + 1]);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < MT; ++x)
+#pragma unroll
+                    for (int r = 0; r < NT; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[MT * c + x][r][e] += acc[x][r][e];
+            }
+        }
+
+        if (flags & kLast) {
+            const bool ends = flags & kEnds, whole = begins && ends;
+            const float vs = F8 ? p.v_scale[u / p.hblocks] : 1.f;
+            const int slot = 2 * worker + (begins ? 1 : 0);
+#pragma unroll
+            for (int r = 0; r < NT; ++r) {
+                const int h = g + 8 * r;
+                float l = sum[r];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                float mul = vs;
+                if (whole) {
+                    const float top = fmaxf(mx[r], sink[r]);
+                    const float f = weight(mx[r], top);
+                    const float tot = top == -INFINITY ? 0.f : l * f + weight(sink[r], top);
+                    mul = tot == 0.f ? 0.f : vs * f / tot;
+                    if (t == 0 && h < heads) {
+                        const int64_t at = int64_t(n) * p.Hq + head0 + h;
+                        p.lse[at] = lse_of(mx[r], top, tot, p.sink, at);
+                    }
+                } else if (t == 0 && h < heads) {
+                    p.part_ml[int64_t(slot) * p.unit_heads + h] = make_float2(mx[r], l);
+                }
+                float* const to = whole ? p.out + (int64_t(n) * p.Hq + head0 + 8 * r) * D
+                                        : p.part_o + (int64_t(slot) * p.unit_heads + 8 * r) * D;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float f = __shfl_sync(0xffffffffu, mul, 8 * t + 4 * e);
+                    const int hc = 2 * t + e;  // this thread's O columns
+                    if (8 * r + hc >= heads) continue;
+#pragma unroll
+                    for (int m = 0; m < D / 16; ++m) {
+                        if constexpr (F8) {
+                            *reinterpret_cast<float2*>(to + hc * D + 16 * m + 2 * g) =
+                                make_float2(o[m][r][e] * f, o[m][r][2 + e] * f);
+                        } else {
+                            to[hc * D + 16 * m + g] = o[m][r][e] * f;
+                            to[hc * D + 16 * m + g + 8] = o[m][r][2 + e] * f;
+                        }
+                    }
+                }
+            }
+            if (begins && !ends) {
+                // the worker of the unit's last tile, which is tiles - 1 - t behind this one
+                const Span sp = span_of<KT>(p, tile.w);
+                const long long rest = sp.tiles - 1 - (tile.z - sp.lo) / KT;
+                rec = Rec{n, u, int(((first + i + rest + 1) * workers - 1) / all) - worker, 0};
+            }
+        }
+    }
+    if (lane == 0) p.rec[worker] = rec;
+}
+
+// Joins the parts of each unit that the even split of the tiles cut. Its parts are the
+// second slot of the worker that began it and the first slots of the next `more` workers,
+// in the order of the keys. Every block lists the cut units from the workers' records; a
+// task is one query head of one of them, and as many warps as there are for each (a power
+// of two, up to a block) share its parts: few long units keep the device as busy as many
+// short ones. Each warp adds its parts in order, then one adds the warps' in order.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams p, int workers,
+                                                                   int block_heads) {
+    constexpr int V = D / 32;  // values of a lane
+    __shared__ int s_owner[kMaxWorkers];
+    __shared__ int s_count[kJoinThreads / 32];
+    __shared__ float s_part[kJoinThreads / 32][D + 2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int WARPS = kJoinThreads / 32;
+    constexpr int PER = (kMaxWorkers + kJoinThreads - 1) / kJoinThreads;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    bool cut[PER];
+    int mine = 0;
+#pragma unroll
+    for (int x = 0; x < PER; ++x) {
+        const int w = tid * PER + x;
+        cut[x] = w < workers && p.rec[w].more > 0;
+        mine += cut[x];
+    }
+    int inc = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += x;
+    }
+    if (lane == 31) s_count[warp] = inc;
+    __syncthreads();
+    int at = inc - mine, owners = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        const int c = s_count[w];
+        if (w < warp) at += c;
+        owners += c;
+    }
+#pragma unroll
+    for (int x = 0; x < PER; ++x)
+        if (cut[x]) s_owner[at++] = tid * PER + x;
+    __syncthreads();
+
+    const int tasks = owners * p.unit_heads;
+    if (tasks == 0) return;
+    int share = 1;  // warps of a task
+    while (share < WARPS && share * 2 * tasks <= int(gridDim.x) * WARPS) share *= 2;
+    const int per_block = WARPS / share, rank = warp % share;
+    for (int base = blockIdx.x * per_block; base < tasks; base += gridDim.x * per_block) {
+        const int task = base + warp / share;
+        float acc[V], m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+        int64_t row = -1;
+        if (task < tasks) {
+            const int owner = s_owner[task / p.unit_heads], h = task % p.unit_heads;
+            const Rec rec = p.rec[owner];
+            const int kvh = rec.u / p.hblocks, hb = rec.u - kvh * p.hblocks;
+            if (hb * block_heads + h < p.group) {
+                row = int64_t(rec.n) * p.Hq + kvh * p.group + hb * block_heads + h;
+                const int parts = rec.more + 1, per = (parts + share - 1) / share;
+                const int end = min(parts, (rank + 1) * per);
+                auto slot = [&](int x) {
+                    return int64_t(x == 0 ? 2 * owner + 1 : 2 * (owner + x)) * p.unit_heads + h;
+                };
+                for (int x0 = rank * per; x0 < end; x0 += 32) {  // 32 parts' weights at a time
+                    const float2 ml = x0 + lane < end ? p.part_ml[slot(x0 + lane)] : make_float2(-INFINITY, 0.f);
+                    float top = ml.x;
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    top = fmaxf(top, m);
+                    const float f = weight(m, top);
+                    float w = weight(ml.x, top);
+                    if (ml.x == -INFINITY) w = 0.f;
+                    m = top;
+                    l *= f;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[e] *= f;
+                    float ls = ml.y * w;
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+                    l += ls;
+                    const int here = min(32, end - x0);
+#pragma unroll 8
+                    for (int x = 0; x < here; ++x) {
+                        const float wx = __shfl_sync(0xffffffffu, w, x);
+                        const float* src = p.part_o + slot(x0 + x) * D + lane * V;
+                        if constexpr (V == 4) {
+                            const float4 y = *reinterpret_cast<const float4*>(src);
+                            acc[0] = fmaf(y.x, wx, acc[0]);
+                            acc[1] = fmaf(y.y, wx, acc[1]);
+                            acc[2] = fmaf(y.z, wx, acc[2]);
+                            acc[3] = fmaf(y.w, wx, acc[3]);
+                        } else {
+                            const float2 y = *reinterpret_cast<const float2*>(src);
+                            acc[0] = fmaf(y.x, wx, acc[0]);
+                            acc[1] = fmaf(y.y, wx, acc[1]);
                         }
                     }
                 }
             }
         }
-        cp_async_wait_group<0>();
-
-        // ---- join the four warps (their rings are free now)
+        if (share > 1) {
+            __syncthreads();
 #pragma unroll
-        for (int r = 0; r < NT; ++r) {
-            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-            if (t == 0) s_ml[warp][g + 8 * r] = make_float2(mx[r], sum[r]);
-        }
-        __syncwarp();
-        float* const mine = reinterpret_cast<float*>(smem + warp * S::REGION);
+            for (int e = 0; e < V; ++e) s_part[warp][lane * V + e] = acc[e];
+            if (lane == 0) {
+                s_part[warp][D] = m;
+                s_part[warp][D + 1] = l;
+            }
+            __syncthreads();
+            if (rank == 0) {
+                float top = m;
+                for (int x = 1; x < share; ++x) top = fmaxf(top, s_part[warp + x][D]);
+                const float f = weight(m, top);
+                l *= f;
 #pragma unroll
-        for (int m = 0; m < D / 16; ++m)
+                for (int e = 0; e < V; ++e) acc[e] *= f;
+                for (int x = 1; x < share; ++x) {
+                    const float w = weight(s_part[warp + x][D], top);
+                    l = fmaf(s_part[warp + x][D + 1], w, l);
 #pragma unroll
-            for (int r = 0; r < NT; ++r)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int h = 8 * r + 2 * t + (i & 1);
-                    const int d = F8 ? 16 * m + 2 * g + (i >> 1) : 16 * m + g + 8 * (i >> 1);
-                    mine[h * S::OROW + d] = o[m][r][i];
+                    for (int e = 0; e < V; ++e) acc[e] = fmaf(s_part[warp + x][lane * V + e], w, acc[e]);
                 }
-        __syncthreads();
-        const bool starts = tile0 == 0, ends = tile1 == sp.tiles;
-        const int slot = 2 * cta + (starts ? 1 : 0);
-        const float vs = F8 ? p.v_scale[kvh] : 1.f;
-        for (int it = tid; it < heads * (D / 4); it += kThreads) {
-            const int h = it / (D / 4), d = (it - h * (D / 4)) * 4;
-            float2 ml[kWarps];
-            float m = -INFINITY;
+                m = top;
+            }
+        }
+        if (rank == 0 && row >= 0) {
+            const float sk = p.sink ? p.sink[row] * kLog2e : -INFINITY;
+            const float top = fmaxf(m, sk);
+            const float f = weight(m, top);
+            const float tot = top == -INFINITY ? 0.f : l * f + weight(sk, top);
+            const float mul = tot == 0.f ? 0.f : f / tot;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                ml[w] = s_ml[w][h];
-                m = fmaxf(m, ml[w].x);
-            }
-            float l = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ml[w].x == m ? 1.f : ex2_approx(ml[w].x - m);
-                const float4 x =
-                    *reinterpret_cast<const float4*>(ofloat + w * (S::REGION / 4) + h * S::OROW + d);
-                l = fmaf(ml[w].y, f, l);
-                acc.x = fmaf(x.x, f, acc.x);
-                acc.y = fmaf(x.y, f, acc.y);
-                acc.z = fmaf(x.z, f, acc.z);
-                acc.w = fmaf(x.w, f, acc.w);
-            }
-            float mul = vs;
-            float* to;
-            const int64_t at = int64_t(n) * p.Hq + head0 + h;
-            if (starts && ends) {
-                const float sk = p.sink ? p.sink[at] * kLog2e : -INFINITY;
-                const float top = fmaxf(m, sk);
-                const float f = m == top ? 1.f : ex2_approx(m - top);
-                const float tot = l * f + (sk == top ? (top == -INFINITY ? 0.f : 1.f) : ex2_approx(sk - top));
-                mul = tot == 0.f ? 0.f : vs * f / tot;
-                to = p.out + at * D + d;
-                if (d == 0) p.lse[at] = lse_of(m, top, tot, p.sink, at);
-            } else {
-                to = p.part_o + (int64_t(slot) * kMaxHeads + h) * D + d;
-                if (d == 0) p.part_ml[int64_t(slot) * kMaxHeads + h] = make_float2(m, l);
-            }
-            *reinterpret_cast<float4*>(to) = make_float4(acc.x * mul, acc.y * mul, acc.z * mul, acc.w * mul);
+            for (int e = 0; e < V; ++e) acc[e] *= mul;
+            float* to = p.out + row * D + lane * V;
+            if constexpr (V == 4) *reinterpret_cast<float4*>(to) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            else *reinterpret_cast<float2*>(to) = make_float2(acc[0], acc[1]);
+            if (lane == 0) p.lse[row] = lse_of(m, top, tot, p.sink, row);
         }
-        if (starts && !ends) {
-            const long long unit_end = base + (long long)(u + 1) * sp.tiles;  // first tile behind the unit
-            rec = Rec{n, u, int((unit_end * ctas - 1) / all) - cta, 0};
-        }
-        pos += nt;
-        if (pos == base + units * sp.tiles) {
-            base = pos;
-            ++n;
-        }
-        __syncthreads();  // the rings may be written again
     }
-    if (tid == 0) p.rec[cta] = rec;
-}
-
-// Joins the parts of each unit that the tiles' even split cut: block (c, h) takes query
-// head h of the unit that CTA c began and did not finish; its other parts are the first
-// ones of CTAs c + 1 .. c + more. Parts are added in the order of the keys.
-template <int D>
-__global__ void __launch_bounds__(D) decode_join_kernel(const DecodeParams p, int block_heads) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x, h = blockIdx.y, d = threadIdx.x;
-    const Rec rec = p.rec[c];
-    if (rec.more == 0) return;
-    const int kvh = rec.u / p.hblocks, hb = rec.u - kvh * p.hblocks;
-    if (hb * block_heads + h >= p.group) return;
-    auto slot = [&](int i) { return int64_t(i == 0 ? 2 * c + 1 : 2 * (c + i)) * kMaxHeads + h; };
-    const int64_t at = int64_t(rec.n) * p.Hq + kvh * p.group + hb * block_heads + h;
-    const float sk = p.sink ? p.sink[at] * kLog2e : -INFINITY;
-    float keys = -INFINITY;
-    for (int i = 0; i <= rec.more; ++i) keys = fmaxf(keys, p.part_ml[slot(i)].x);
-    const float m = fmaxf(keys, sk);
-    float l = sk == m ? (m == -INFINITY ? 0.f : 1.f) : ex2_approx(sk - m);
-    float acc = 0.f;
-#pragma unroll 4
-    for (int i = 0; i <= rec.more; ++i) {
-        const float2 ml = p.part_ml[slot(i)];
-        const float f = ml.x == m ? 1.f : ex2_approx(ml.x - m);
-        l = fmaf(ml.y, f, l);
-        acc = fmaf(p.part_o[slot(i) * D + d], f, acc);
-    }
-    p.out[at * D + d] = l == 0.f ? 0.f : acc / l;
-    if (d == 0) p.lse[at] = lse_of(keys, m, l, p.sink, at);
 }
 
 // --------------------------------------------------------------------------
@@ -619,13 +785,14 @@ __global__ void __launch_bounds__(D) decode_join_kernel(const DecodeParams p, in
 struct Layout {
     size_t rec, ml, o, total;
 };
-Layout layout_of(int64_t D) {
+Layout layout_of(int64_t D, int64_t group) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const size_t rows = size_t(2) * kMaxWorkers * (group < 16 ? group : 16);
     Layout l{};
     l.rec = 0;
-    l.ml = up(kMaxCtas * sizeof(Rec));
-    l.o = up(l.ml + size_t(2) * kMaxCtas * kMaxHeads * sizeof(float2));
-    l.total = up(l.o + size_t(2) * kMaxCtas * kMaxHeads * D * 4);
+    l.ml = up(kMaxWorkers * sizeof(Rec));
+    l.o = up(l.ml + rows * sizeof(float2));
+    l.total = up(l.o + rows * D * 4);
     return l;
 }
 
@@ -639,8 +806,9 @@ inkling_status check_decode(const inkling_kv_cache_desc* c, const inkling_rel_at
     if (d->requests >= (int64_t(1) << 24) || d->heads_q >= 65536 || d->rel_extent >= lim || d->window >= lim ||
         d->max_pages >= lim || d->max_pages * c->page_size >= lim)
         return INKLING_ERR_UNSUPPORTED;
-    // the tiles are numbered through in 64 bits, times the CTAs
-    if (d->requests * d->heads_q >= (int64_t(1) << 50) / (d->max_pages * c->page_size + 1))
+    if (d->rel_extent % 8 != 0) return INKLING_ERR_UNSUPPORTED;  // profile rows are copied 16 bytes at a time
+    // a worker counts its tiles in 32 bits
+    if (d->requests * d->heads_q >= (int64_t(1) << 40) / (d->max_pages * c->page_size + 1))
         return INKLING_ERR_UNSUPPORTED;
     return INKLING_OK;
 }
@@ -650,6 +818,7 @@ inkling_status status_of(cudaError_t e) { return note_cuda_error(e) == cudaSucce
 template <class S>
 cudaError_t launch_decode(DecodeParams& p, cudaStream_t st) {
     p.hblocks = (p.group + 8 * S::NT - 1) / (8 * S::NT);
+    p.unit_heads = p.group < 8 * S::NT ? p.group : 8 * S::NT;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -658,24 +827,24 @@ cudaError_t launch_decode(DecodeParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     // at most the tiles of a full table
     const int span = p.W > 0 && p.W < p.cap ? p.W : p.cap;
-    const int64_t unit_tiles = (span + S::CT - 1) / S::CT;
-    const int64_t tiles = int64_t(p.N) * p.Hkv * p.hblocks * unit_tiles;
+    const int64_t unit_tiles = (span + S::KT - 1) / S::KT;
+    const int64_t workers = (int64_t(p.N) * p.Hkv * p.hblocks * unit_tiles + kMinTiles - 1) / kMinTiles;
     int64_t grid = int64_t(sms) * kCtasPerSm;
     if (grid > kMaxCtas) grid = kMaxCtas;
-    if (grid > tiles) grid = tiles;
+    if (grid > workers) grid = workers;
     decode_kernel<S><<<unsigned(grid), kThreads, S::SMEM, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess || unit_tiles == 1) return e;  // units of one tile are never cut
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(grid), 8 * S::NT < p.group ? 8 * S::NT : p.group);
-    cfg.blockDim = dim3(S::D);
+    cfg.gridDim = dim3(unsigned(sms));
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_join_kernel<S::D>, DecodeParams(p), 8 * S::NT);
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel<S::D>, DecodeParams(p), int(grid) * kWarps, 8 * S::NT);
 }
 
 template <int D, bool F8>
@@ -693,7 +862,7 @@ size_t inkling_rel_attn_decode_workspace_size(const inkling_kv_cache_desc* cache
                                               const inkling_rel_attn_decode_dims* dims) {
     CacheLayout lay;
     if (check_decode(cache, dims, &lay) != INKLING_OK) return 0;
-    return layout_of(cache->head_dim).total;
+    return layout_of(cache->head_dim, dims->heads_q / cache->heads_kv).total;
 }
 
 inkling_status inkling_rel_attn_decode(const inkling_kv_cache_desc* cache, const inkling_rel_attn_decode_dims* dims,
@@ -715,7 +884,7 @@ inkling_status inkling_rel_attn_decode(const inkling_kv_cache_desc* cache, const
         !aligned(sink, 4) || !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(lse, 4))
         return INKLING_ERR_INVALID_ARG;
     const int64_t D = cache->head_dim;
-    const Layout l = layout_of(D);
+    const Layout l = layout_of(D, dims->heads_q / cache->heads_kv);
     if (workspace_bytes < l.total) return INKLING_ERR_INVALID_ARG;
 
     DecodeParams p{};
@@ -729,6 +898,12 @@ inkling_status inkling_rel_attn_decode(const inkling_kv_cache_desc* cache, const
     p.P = int(cache->page_size);
     p.num_pages = int(cache->num_pages);
     p.cap = int(dims->max_pages * cache->page_size);
+    // j / P for j < 2^31 by a multiplication (Granlund and Montgomery): with 2^s >= P and
+    // m = floor(2^(31+s) / P) + 1, m P - 2^(31+s) <= 2^s, so j m >> (31 + s) is exact
+    uint32_t shift = 0;
+    while ((int64_t(1) << shift) < p.P) ++shift;
+    p.p_mul = uint32_t((uint64_t(1) << (31 + shift)) / uint64_t(p.P) + 1);
+    p.p_shift = 31 + shift;
     const int64_t es = lay.e4m3 ? 1 : 2;
     p.page_stride = lay.page_stride * es;
     p.token_stride = lay.token_stride * es;

@@ -54,7 +54,7 @@ def test_strides_of_single_extents_are_not_looked_at(lib):
 @pytest.mark.parametrize("bad,expect", [
     (dict(requests=-1), 1), (dict(heads_q=0), 1), (dict(heads_q=6), 1), (dict(rel_extent=-8), 1), (dict(window=-1), 1),
     (dict(max_pages=0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(requests=1 << 24), 2),
-    (dict(heads_q=65536), 2), (dict(rel_extent=1 << 30), 2), (dict(window=1 << 30), 2), (dict(max_pages=1 << 26), 2),
+    (dict(heads_q=65536), 2), (dict(rel_extent=1 << 30), 2), (dict(rel_extent=12), 2), (dict(window=1 << 30), 2), (dict(max_pages=1 << 26), 2),
     (dict(requests=1 << 23, max_pages=1 << 24), 2)])
 def test_decode_sizes(lib, bad, expect):
     d = dec(**bad)

@@ -82,6 +82,15 @@ def problem(lens, hq, hkv, d, page, r, dtype="bf16", layout="nhd", seed=0, max_p
     return x, dict(k_scale=ks, v_scale=vs)
 
 
+def workspace(x, fill):
+    from learned_relative_gqa_b200 import binding
+    N, Hq, _ = x["q"].shape
+    R = 0 if x["profiles"] is None else x["profiles"].shape[2]
+    ws = binding.alloc_decode_workspace(binding.make_kv_cache_desc(x["k_cache"], x["v_cache"]),
+                                        binding.DecodeDims(N, Hq, R, 0, x["block_table"].shape[1], 0.0), "cuda")
+    return ws.fill_(fill)
+
+
 def f64(t):
     return None if t is None else t.cpu().double().numpy()
 
@@ -227,7 +236,7 @@ def test_decode_equal_calls_give_equal_bits():
     from learned_relative_gqa_b200 import binding
     x, s = problem([1500, 3, 700, 0], 16, 2, 128, 16, 64, seed=13)
     a = binding.paged_decode(**x, **s)
-    ws = torch.full((8 << 20,), 0xAB, dtype=torch.uint8, device="cuda")  # what a workspace holds means nothing
+    ws = workspace(x, 0xAB)  # what a workspace holds means nothing
     for _ in range(5):
         b = binding.paged_decode(**x, **s, workspace=ws)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
@@ -274,7 +283,7 @@ def test_decode_captured_and_replayed_with_other_lengths():
     x, s = problem(lens, 8, 2, 128, 16, 64, seed=16, poison=False)
     binding.paged_decode(**x, **s)
     graphs = []
-    ws = torch.empty(8 << 20, dtype=torch.uint8, device="cuda")
+    ws = workspace(x, 0)
     for window in (0, 100):  # two graphs that share a workspace, replayed in turn
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
