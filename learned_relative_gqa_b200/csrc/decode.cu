@@ -37,6 +37,7 @@
 // scales stay outside the products. q (BF16) is first multiplied by a power of two per
 // head that brings its largest value into [1, 2): exact but for values below 2^-14 of
 // the largest, whose error (2^-25 of it) is under the FP32 sum's own.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -57,11 +58,17 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 320;
 constexpr int kMaxWorkers = kMaxCtas * kWarps;  // workspace slots: two per worker
-constexpr int kMinTiles = 2;                    // tiles that a worker takes at least, where there are enough
-constexpr int kJoinThreads = 1024;
+// One CTA per unit, with no split, up to these sizes: tiles of a unit and units of the call.
+constexpr int kWholeTiles = 32;
+constexpr int kWholeUnits = 1024;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBatch = 6;                   // parts that a lane of it loads at once
 
-struct Rec {  // a worker's last unit, if it began there and did not end: its other parts are
-    int n, u, more, pad;  // the first ones of the next `more` workers
+// A worker's last unit, if it began there and did not end: first row of out, rows, and how
+// many of the next workers have the unit's other parts (their first ones).
+struct alignas(16) Rec {
+    long long row;
+    int heads, more;
 };
 
 struct DecodeParams {
@@ -112,11 +119,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// two e4m3 codes (low and high byte) as an FP16 pair, exactly
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(codes)));
-    return r;
+// four e4m3 codes as two FP16 pairs, exactly
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
 }
 
 template <bool F16>
@@ -149,7 +156,15 @@ struct Shape {
     static constexpr int SIDE = KT * RB;                    // bytes of K (or V) in a stage
     static constexpr int BCH = KT / 8 + 1;                  // 16-byte chunks that hold KT profile entries
     static constexpr int STAGE = 2 * SIDE + 8 * NT * BCH * 16;
-    static constexpr int SMEM = kWarps * STAGES * STAGE;
+    // Tiles (and unit starts) that a worker takes at least. A part is written and read again,
+    // 1 KB for each head: no more parts than their traffic stays around half of the tiles'.
+    // Measured with one request (GPU time): 4096 tokens, 8 x 4 heads 11.6 us with 2 and
+    // 13.1 us with 4; 32768 tokens, 1 x 16 heads 22.1 us with 2 and 18.5 us with 4.
+    static constexpr int MIN_TILES = 2 * NT;
+    static constexpr int RING = STAGES * STAGE;
+    static constexpr int SMEM = kWarps * RING;
+    static constexpr int OROW = D + 4;                      // floats of a head's row when warps join (no bank conflicts)
+    static_assert(8 * NT * OROW * 4 <= RING, "the rings hold the warps' results when they join");
     // chunk c of row r stands at chunk c ^ swz(r): ldmatrix's eight rows use all banks
     __device__ static __forceinline__ int swz(int row) { return RB >= 128 ? (row & 7) : ((row >> 1) & 3); }
 };
@@ -182,90 +197,122 @@ __device__ __forceinline__ float weight(float x, float top) { return x == top ? 
 
 enum : int { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8 };  // of a run of tiles of one unit
 
-// Position in the numbered tiles: request, unit of it, tile of that.
+// Position in the numbered tiles: request, unit of it, tile of that; `at` counts tiles and
+// unit starts from the worker's first one.
 struct Cursor {
     Span s;
-    int n, u, t, next_len;
+    int n, u, t, next_len, at;
 };
 
-template <class S>
+// WHOLE: a CTA for each unit and no split. Its warps take the unit's tiles in turn and join
+// through shared memory: no prefix sums at the start, no second kernel at the end.
+// Otherwise the grid's warps are workers with an even share each of all tiles. A unit counts
+// one more than its tiles there, which is about what loading its query and writing its
+// result take, so that runs of short requests are not the last to finish.
+template <class S, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __grid_constant__ DecodeParams p) {
     constexpr int D = S::D, NT = S::NT, KT = S::KT, ST = S::STAGES;
     constexpr bool F8 = S::F8;
     constexpr int NS = KT / 8;  // S accumulator tiles of 8 keys
+    constexpr int STEP = WHOLE ? kWarps : 1;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int4 s_tile[kWarps][ST];    // request, unit, first key, length
-    __shared__ uint2 s_flags[kWarps][ST];  // allowed keys of the tile, kFirst ..
+    __shared__ int4 s_flags[kWarps][ST];   // allowed keys of the tile, kFirst .., Cursor::at
     __shared__ long long s_sum[kWarps];
     __shared__ long long s_base[kWarps];
-    __shared__ int s_n[kWarps];
+    __shared__ int s_n[kWarps], s_len[kWarps];
+    __shared__ float2 s_ml[kWarps][8 * NT];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
-    // the joining kernel may be set up now; it waits for this one's results itself
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    // ---- this worker's run of tiles
     const int units = p.Hkv * p.hblocks;  // per request
-    const int chunk = (p.N + kThreads - 1) / kThreads;
-    const int n0 = min(tid * chunk, p.N), n1 = min(n0 + chunk, p.N);
-    long long own = 0;
-    for (int n = n0; n < n1; ++n) own += span_of<KT>(p, p.lens[n]).tiles;
-    long long inc = own;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += x;
-    }
-    if (lane == 31) s_sum[warp] = inc;
-    __syncthreads();
-    long long before = inc - own, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += s_sum[w];
-        all += s_sum[w];
-    }
-    all *= units;
-    before *= units;
-    const long long enough = (all + kMinTiles - 1) / kMinTiles;
-    const int workers = int(enough < (long long)gridDim.x * kWarps ? enough : (long long)gridDim.x * kWarps);
-    // neighbours in the order of the tiles are on different SMs
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const long long first = (long long)(w * gridDim.x + blockIdx.x) * all / workers;
-        if (before <= first && first < before + own * units) {
-            long long at = before;
-            int n = n0;
-            for (;; ++n) {
-                const long long size = (long long)span_of<KT>(p, p.lens[n]).tiles * units;
-                if (first < at + size) break;
-                at += size;
-            }
-            s_n[w] = n;
-            s_base[w] = at;
-        }
-    }
-    __syncthreads();
-    const int worker = warp * gridDim.x + blockIdx.x;
-    if (worker >= workers) {
-        if (lane == 0) p.rec[worker] = Rec{0, 0, 0, 0};
-        return;
-    }
-    const long long first = worker * all / workers;
-    const int total = int((worker + 1) * all / workers - first);
+    const uint32_t ring = smem_u32(smem) + warp * S::RING;
 
-    const uint32_t ring = smem_u32(smem) + warp * ST * S::STAGE;
+    Cursor cur{};
+    long long all = 0, first = 0;
+    int limit = 0, worker = 0, workers = 0;
+    if constexpr (WHOLE) {
+        cur.n = blockIdx.x / units;
+        cur.u = blockIdx.x - cur.n * units;
+        cur.t = warp;
+        cur.s = span_of<KT>(p, p.lens[cur.n]);
+    } else {
+        // the joining kernel may be set up now; it waits for this one's results itself
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        const int chunk = (p.N + kThreads - 1) / kThreads;
+        const int n0 = min(tid * chunk, p.N), n1 = min(n0 + chunk, p.N);
+        long long own = 0;
+        for (int n = n0; n < n1; ++n) own += span_of<KT>(p, p.lens[n]).tiles + 1;
+        long long inc = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += x;
+        }
+        if (lane == 31) s_sum[warp] = inc;
+        __syncthreads();
+        long long before = inc - own;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += s_sum[w];
+            all += s_sum[w];
+        }
+        all *= units;
+        before *= units;
+        const long long enough = max(all / S::MIN_TILES, 1ll);
+        workers = int(enough < (long long)gridDim.x * kWarps ? enough : (long long)gridDim.x * kWarps);
+        // neighbours in the order of the tiles are on different SMs
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const long long from = (long long)(w * gridDim.x + blockIdx.x) * all / workers;
+            if (before <= from && from < before + own * units) {
+                long long at = before;
+                int n = n0, len;
+                for (;; ++n) {
+                    len = p.lens[n];
+                    const long long size = (long long)(span_of<KT>(p, len).tiles + 1) * units;
+                    if (from < at + size) break;
+                    at += size;
+                }
+                s_n[w] = n;
+                s_len[w] = len;
+                s_base[w] = at;
+            }
+        }
+        __syncthreads();
+        worker = warp * gridDim.x + blockIdx.x;
+        if (worker >= workers) {
+            if (lane == 0) p.rec[worker] = Rec{0, 0, 0};
+            return;
+        }
+        first = worker * all / workers;
+        limit = int((worker + 1) * all / workers - first);
+        cur.n = s_n[warp];
+        cur.next_len = cur.n + 1 < p.N ? p.lens[cur.n + 1] : 0;
+        cur.s = span_of<KT>(p, s_len[warp]);
+        const long long local = first - s_base[warp];
+        cur.u = int(local / (cur.s.tiles + 1));
+        cur.t = int(local - (long long)cur.u * (cur.s.tiles + 1)) - 1;
+        if (cur.t < 0) cur.t = 0, cur.at = 1;  // the range begins with the unit's start
+    }
 
     // ---- producer: lane r < KT looks key r of a tile up, all lanes copy
+    constexpr uint32_t kAll = KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1u;
     const int my_key = lane & (KT - 1);
+    auto there = [&](const Cursor& c) { return WHOLE ? c.t < c.s.tiles : c.at < limit; };
     auto advance = [&](Cursor& c) {
-        if (++c.t < c.s.tiles) return;
-        c.t = 0;
-        if (++c.u < units) return;
-        c.u = 0;
-        ++c.n;
-        c.s = span_of<KT>(p, c.next_len);
-        c.next_len = c.n + 1 < p.N ? p.lens[c.n + 1] : 0;
+        c.t += STEP;
+        if constexpr (!WHOLE) {
+            ++c.at;
+            if (c.t < c.s.tiles) return;
+            c.t = 0;
+            ++c.at;
+            if (++c.u < units) return;
+            c.u = 0;
+            ++c.n;
+            c.s = span_of<KT>(p, c.next_len);
+            c.next_len = c.n + 1 < p.N ? p.lens[c.n + 1] : 0;
+        }
     };
     auto lookup = [&](const Cursor& c) {  // -1: not allowed
         const int j = c.s.lo + c.t * KT + my_key;
@@ -276,26 +323,43 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
         const int kvh = c.u / p.hblocks, hb = c.u - kvh * p.hblocks;
         const int head0 = kvh * p.group + hb * 8 * NT;
         const bool ok = page >= 0 && page < p.num_pages;
-        const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-        const bool run = i == 0 || c.t == 0;
+        const uint32_t mask = __ballot_sync(0xffffffffu, ok) & kAll;
+        const bool run = i == 0 || (!WHOLE && c.t == 0), ends = c.t == c.s.tiles - 1;
         if (lane == 0) {
             s_tile[warp][stage] = make_int4(c.n, c.u, j0, c.s.len);
-            s_flags[warp][stage] =
-                make_uint2(mask, (run ? kFirst : 0) | (i == total - 1 || c.t == c.s.tiles - 1 ? kLast : 0) |
-                                     (c.t == 0 ? kBegins : 0) | (c.t == c.s.tiles - 1 ? kEnds : 0));
+            s_flags[warp][stage] = make_int4(int(mask),
+                                             (run ? kFirst : 0) | (ends || c.at + 1 >= limit ? kLast : 0) |
+                                                 (c.t == 0 ? kBegins : 0) | (ends ? kEnds : 0),
+                                             c.at, 0);
         }
-        const int64_t at = ok ? int64_t(page) * p.page_stride +
-                                    int64_t(j - page_index(p, j) * p.P) * p.token_stride + kvh * p.head_stride
-                              : 0;
         const uint32_t dst = ring + stage * S::STAGE;
+        const int offset = j - page_index(p, j) * p.P;  // in its page
+        int64_t at = ok ? int64_t(page) * p.page_stride + int64_t(offset) * p.token_stride + kvh * p.head_stride : 0;
+        constexpr int ROWS = 32 / S::CPR;  // of a copy of 16 bytes per lane
+        const int r0 = lane / S::CPR, ch = lane % S::CPR;
+        if (mask == kAll && __shfl_sync(0xffffffffu, offset, 0) + KT <= p.P) {
+            // the usual tile: every key allowed, all in one page, so rows follow each other
+            at = __shfl_sync(0xffffffffu, at, 0) + r0 * p.token_stride + ch * 16;
+            const uint8_t *k = p.k_cache + at, *v = p.v_cache + at;
 #pragma unroll
-        for (int x = 0; x < KT * S::CPR / 32; ++x) {
-            const int r = x * (32 / S::CPR) + lane / S::CPR, ch = lane % S::CPR;
-            const int64_t off = __shfl_sync(0xffffffffu, at, r) + ch * 16;
-            const uint32_t bytes = (mask >> r) & 1u ? 16u : 0u;
-            const uint32_t to = dst + r * S::RB + ((ch ^ S::swz(r)) << 4);
-            cp_async_16(to, p.k_cache + off, bytes);
-            cp_async_16(to + S::SIDE, p.v_cache + off, bytes);
+            for (int x = 0; x < KT / ROWS; ++x) {
+                const int r = x * ROWS + r0;
+                const uint32_t to = dst + r * S::RB + ((ch ^ S::swz(r)) << 4);
+                cp_async_16(to, k, 16u);
+                cp_async_16(to + S::SIDE, v, 16u);
+                k += ROWS * p.token_stride;
+                v += ROWS * p.token_stride;
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < KT / ROWS; ++x) {
+                const int r = x * ROWS + r0;
+                const int64_t off = __shfl_sync(0xffffffffu, at, r) + ch * 16;
+                const uint32_t bytes = (mask >> r) & 1u ? 16u : 0u;
+                const uint32_t to = dst + r * S::RB + ((ch ^ S::swz(r)) << 4);
+                cp_async_16(to, p.k_cache + off, bytes);
+                cp_async_16(to + S::SIDE, p.v_cache + off, bytes);
+            }
         }
         // profile entries of the distances [dlo, dlo + KT), in whole chunks of 8
         const int dlo = c.s.len - KT - j0;
@@ -310,136 +374,165 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
                 cp_async_16(dst + 2 * S::SIDE + x * 16, p.profiles + off, in ? 16u : 0u);
             }
         }
-        if (run) {  // q and the sink are loaded when the tile's turn comes: warm L2 for that
+        if (!WHOLE && run) {  // q and the sink are loaded when the tile's turn comes: warm L2 for that
             if (lane < heads * D / 64) prefetch_l2(p.q + (int64_t(c.n) * p.Hq + head0) * D + lane * 64);
             if (lane == 31 && p.sink) prefetch_l2(p.sink + int64_t(c.n) * p.Hq + head0);
         }
     };
 
-    Cursor cur;
+    // ---- query of a unit: fragments (BF16 pairs as they stand in memory) and the sink
+    struct Query {
+        uint32_t a[D / 16][2 * NT];
+        float sink[NT];
+    };
+    int head0 = 0, heads = 0;
+    auto place = [&](int u) {
+        const int kvh = u / p.hblocks, hb = u - kvh * p.hblocks;
+        head0 = kvh * p.group + hb * 8 * NT;
+        heads = min(8 * NT, p.group - hb * 8 * NT);
+    };
+    auto load_query = [&](Query& q, int n, int from, int count) {
+#pragma unroll
+        for (int r = 0; r < NT; ++r) {
+            const int h = g + 8 * r;
+            const int64_t at = int64_t(n) * p.Hq + from + h;
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + at * D);
+            q.sink[r] = p.sink && h < count ? p.sink[at] : -INFINITY;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                // BF16: columns 16 ks + {2t, 2t+1} and + 8; e4m3: 16 ks + {4t .. 4t+3}, the
+                // order in which a code word holds them (K uses the same one)
+                const int w0 = F8 ? 8 * ks + 2 * t : 8 * ks + t, w1 = F8 ? w0 + 1 : w0 + 4;
+                q.a[ks][2 * r] = h < count ? src[w0] : 0u;
+                q.a[ks][2 * r + 1] = h < count ? src[w1] : 0u;
+            }
+        }
+    };
+
+    Query qa;
+    float zscale[NT];
+    float o[D / 16][NT][4];
+    float mx[NT], sum[NT];
+    auto start = [&](int u) {  // of a unit, its query in qa
+#pragma unroll
+        for (int r = 0; r < NT; ++r) {
+            zscale[r] = p.scale_log2;
+            qa.sink[r] *= kLog2e;
+            mx[r] = -INFINITY;
+            sum[r] = 0.f;
+            if constexpr (F8) {
+                float top = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 x = unpack2<false>(qa.a[ks][2 * r + e]);
+                        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^e <= top < 2^(e+1) (zero, subnormal and infinite rows: the nearest normal power)
+                const int e = min(max(int(__float_as_uint(top) >> 23) - 127, -126), 126);
+                const float down = __uint_as_float(uint32_t(127 - e) << 23);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float2 x = unpack2<false>(qa.a[ks][2 * r + y]);
+                        qa.a[ks][2 * r + y] = pack2<true>(x.x * down, x.y * down);
+                    }
+                zscale[r] *= __uint_as_float(uint32_t(127 + e) << 23) * p.k_scale[u / p.hblocks];
+            }
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[m][r][e] = 0.f;
+        }
+    };
+
+    if constexpr (WHOLE) {
+        place(cur.u);
+        load_query(qa, cur.n, head0, heads);
+    }
     int page = -1, made = 0;
     {
-        cur.n = s_n[warp];
-        cur.s = span_of<KT>(p, p.lens[cur.n]);
-        cur.next_len = cur.n + 1 < p.N ? p.lens[cur.n + 1] : 0;
-        const long long local = first - s_base[warp];
-        cur.u = int(local / cur.s.tiles);
-        cur.t = int(local - (long long)cur.u * cur.s.tiles);
         // the first lookups go out together
         Cursor at[ST];
         int pages[ST];
 #pragma unroll
         for (int i = 0; i < ST; ++i) {
             at[i] = cur;
-            pages[i] = -1;
-            if (i < total) {
-                if (i > 0) {
-                    at[i] = at[i - 1];
-                    advance(at[i]);
-                }
-                pages[i] = lookup(at[i]);
+            if (i > 0) {
+                at[i] = at[i - 1];
+                if (there(at[i - 1])) advance(at[i]);
             }
+            pages[i] = there(at[i]) ? lookup(at[i]) : -1;
         }
 #pragma unroll
         for (int i = 0; i < ST - 1; ++i) {
-            if (i < total) issue(at[i], i, i, pages[i]);
+            if (there(at[i])) issue(at[i], made++, i, pages[i]);
             cp_async_commit();
         }
-        made = min(ST - 1, total);
         cur = at[ST - 1];
         page = pages[ST - 1];
     }
+    if constexpr (WHOLE) start(cur.u);
 
-    uint32_t qa[D / 16][2 * NT];
-    float zscale[NT], sink[NT];
-    float o[D / 16][NT][4];
-    float mx[NT], sum[NT];
-    int head0 = 0, heads = 0;
-    bool begins = false;
-    Rec rec{0, 0, 0, 0};
+    [[maybe_unused]] Query qn;  // the next unit's query, where registers allow
+    [[maybe_unused]] bool begins = false;
+    Rec rec{0, 0, 0};
 
     int stage = 0;
-    for (int i = 0; i < total; ++i) {
+    for (int i = 0; i < made; ++i) {
         cp_async_wait_group<ST - 2>();
         __syncwarp();  // the tile is in, and every lane is done with the previous one's stage
-        if (made < total) {
-            issue(cur, made, stage == 0 ? ST - 1 : stage - 1, page);
-            if (++made < total) {
-                advance(cur);
-                page = lookup(cur);
-            }
-        }
-        cp_async_commit();
-
+        const int behind = stage == 0 ? ST - 1 : stage - 1, ahead = stage == ST - 1 ? 0 : stage + 1;
+        const bool had_next = i + 1 < made;
         const int4 tile = s_tile[warp][stage];
-        const uint32_t mask = s_flags[warp][stage].x, flags = s_flags[warp][stage].y;
-        const int n = tile.x, u = tile.y;
+        const int4 info = s_flags[warp][stage];
+        const uint32_t mask = uint32_t(info.x);
+        const int flags = info.y;
         const uint32_t kbase = ring + stage * S::STAGE, vbase = kbase + S::SIDE, bbase = vbase + S::SIDE;
-        stage = stage == ST - 1 ? 0 : stage + 1;
 
-        if (flags & kFirst) {
-            begins = flags & kBegins;
-            const int kvh = u / p.hblocks, hb = u - kvh * p.hblocks;
-            head0 = kvh * p.group + hb * 8 * NT;
-            heads = min(8 * NT, p.group - hb * 8 * NT);
-#pragma unroll
-            for (int r = 0; r < NT; ++r) {
-                const int h = g + 8 * r;
-                const int64_t at = int64_t(n) * p.Hq + head0 + h;
-                const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + at * D);
-                zscale[r] = p.scale_log2;
-                sink[r] = p.sink && h < heads ? p.sink[at] * kLog2e : -INFINITY;
-                mx[r] = -INFINITY;
-                sum[r] = 0.f;
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    // BF16: columns 16 ks + {2t, 2t+1} and + 8; e4m3: 16 ks + {4t .. 4t+3}, the
-                    // order in which a code word holds them (K uses the same one)
-                    const int w0 = F8 ? 8 * ks + 2 * t : 8 * ks + t, w1 = F8 ? w0 + 1 : w0 + 4;
-                    qa[ks][2 * r] = h < heads ? src[w0] : 0u;
-                    qa[ks][2 * r + 1] = h < heads ? src[w1] : 0u;
-                }
-                if constexpr (F8) {
-                    float top = 0.f;
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float2 x = unpack2<false>(qa[ks][2 * r + e]);
-                            top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
-                        }
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    // 2^e <= top < 2^(e+1) (zero, subnormal and infinite rows: the nearest normal power)
-                    const int e = min(max(int(__float_as_uint(top) >> 23) - 127, -126), 126);
-                    const float down = __uint_as_float(uint32_t(127 - e) << 23);
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const float2 x = unpack2<false>(qa[ks][2 * r + y]);
-                            qa[ks][2 * r + y] = pack2<true>(x.x * down, x.y * down);
-                        }
-                    zscale[r] *= __uint_as_float(uint32_t(127 + e) << 23) * p.k_scale[kvh];
-                }
-#pragma unroll
-                for (int m = 0; m < D / 16; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[m][r][e] = 0.f;
+        if constexpr (!WHOLE) {
+            if (flags & kFirst) {
+                begins = flags & kBegins;
+                place(tile.y);
+                if (NT == 1 && i > 0) qa = qn;
+                else load_query(qa, tile.x, head0, heads);
+                start(tile.y);
+            }
+            // one group of heads leaves the registers to have the next unit's query on its way
+            if (NT == 1 && had_next && (s_flags[warp][ahead].y & kFirst)) {
+                const int4 next = s_tile[warp][ahead];
+                const int kvh = next.y / p.hblocks, hb = next.y - kvh * p.hblocks;
+                load_query(qn, next.x, kvh * p.group + hb * 8 * NT, min(8 * NT, p.group - hb * 8 * NT));
             }
         }
+        stage = ahead;
 
-        if (mask != 0) {
+        // The next tile's copies are issued behind the first product, whose latency they hide in.
+        auto produce = [&] {
+            if (there(cur)) {
+                issue(cur, made++, behind, page);
+                advance(cur);
+                if (there(cur)) page = lookup(cur);
+            }
+            cp_async_commit();
+        };
+        if (mask == 0) {
+            produce();
+        } else {
             // lane's row and chunk parity in the 16-key ldmatrix of either side
             const int lrow = (lane & 7) + ((lane >> 4) << 3), lch = (lane >> 3) & 1;
             const int lswz = S::swz(lane & 7);
 
-            // ---- S = Q K^T
-            float s[NS][4];
+            // ---- S = Q K^T, in two sums to halve the chain of dependent products
+            float s[NS][4], s2[NS][4];
 #pragma unroll
             for (int x = 0; x < NS; ++x)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[x][e] = 0.f;
+                for (int e = 0; e < 4; ++e) s[x][e] = s2[x][e] = 0.f;
 #pragma unroll
             for (int c = 0; c < S::CPR / 2; ++c) {  // pairs of 16-byte chunks
 #pragma unroll
@@ -447,22 +540,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
                     uint32_t f[4];
                     ldmatrix_x4(kbase + (kk * 16 + lrow) * S::RB + (((2 * c + lch) ^ lswz) << 4), f);
                     if constexpr (!F8) {
-                        const uint32_t a1 = NT == 2 ? qa[c][2 * (NT - 1)] : 0u, a3 = NT == 2 ? qa[c][2 * NT - 1] : 0u;
-                        mma16816<false>(s[2 * kk], qa[c][0], a1, qa[c][1], a3, f[0], f[1]);
-                        mma16816<false>(s[2 * kk + 1], qa[c][0], a1, qa[c][1], a3, f[2], f[3]);
+                        const uint32_t a1 = NT == 2 ? qa.a[c][2 * (NT - 1)] : 0u, a3 = NT == 2 ? qa.a[c][2 * NT - 1] : 0u;
+                        float(&to)[NS][4] = c % 2 ? s2 : s;
+                        mma16816<false>(to[2 * kk], qa.a[c][0], a1, qa.a[c][1], a3, f[0], f[1]);
+                        mma16816<false>(to[2 * kk + 1], qa.a[c][0], a1, qa.a[c][1], a3, f[2], f[3]);
                     } else {
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {  // the pair's two chunks: 16 columns each
-                            const uint32_t* a = qa[2 * c + x];
+                            const uint32_t* a = qa.a[2 * c + x];
                             const uint32_t a1 = NT == 2 ? a[2 * (NT - 1)] : 0u, a3 = NT == 2 ? a[2 * NT - 1] : 0u;
-                            mma16816<true>(s[2 * kk], a[0], a1, a[1], a3, e4m3x2_to_f16x2(f[x]),
-                                           e4m3x2_to_f16x2(f[x] >> 16));
-                            mma16816<true>(s[2 * kk + 1], a[0], a1, a[1], a3, e4m3x2_to_f16x2(f[x + 2]),
-                                           e4m3x2_to_f16x2(f[x + 2] >> 16));
+                            float(&to)[NS][4] = x ? s2 : s;
+                            uint32_t b0, b1, b2, b3;
+                            e4m3x4_to_f16x4(f[x], b0, b1);
+                            e4m3x4_to_f16x4(f[x + 2], b2, b3);
+                            mma16816<true>(to[2 * kk], a[0], a1, a[1], a3, b0, b1);
+                            mma16816<true>(to[2 * kk + 1], a[0], a1, a[1], a3, b2, b3);
                         }
                     }
                 }
             }
+            produce();
 
             // ---- logits in log2 units, their maximum, the running state
 #pragma unroll
@@ -470,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
 #pragma unroll
                 for (int x = 0; x < NS; ++x)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) s[x][2 * r + e] *= zscale[r];
+                    for (int e = 0; e < 2; ++e) s[x][2 * r + e] = (s[x][2 * r + e] + s2[x][2 * r + e]) * zscale[r];
             const int dlo = tile.w - KT - tile.z;
             if (p.R > 0 && dlo < p.R) {
 #pragma unroll
@@ -485,18 +582,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
                                                    s[x][2 * r + e]);
                 }
             }
+            if (mask != kAll) {
+#pragma unroll
+                for (int r = 0; r < NT; ++r)
+#pragma unroll
+                    for (int x = 0; x < NS; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (!((mask >> (8 * x + 2 * t + e)) & 1u)) s[x][2 * r + e] = -INFINITY;
+            }
             float top[NT];
             bool grows = false;
 #pragma unroll
             for (int r = 0; r < NT; ++r) {
                 top[r] = -INFINITY;
 #pragma unroll
-                for (int x = 0; x < NS; ++x)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (!((mask >> (8 * x + 2 * t + e)) & 1u)) s[x][2 * r + e] = -INFINITY;
-                        top[r] = fmaxf(top[r], s[x][2 * r + e]);
-                    }
+                for (int x = 0; x < NS; ++x) top[r] = fmax3(top[r], s[x][2 * r], s[x][2 * r + 1]);
                 top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
                 top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
                 grows |= top[r] > mx[r] + kRescaleThreshold;
@@ -558,11 +659,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
                         uint32_t a0 = f[0], a1 = f[1], a2 = f[2], a3 = f[3];
                         if constexpr (F8) {
                             // a 16-bit unit holds columns 2g, 2g + 1 of one key: regroup by column
-                            const uint32_t w0 = __byte_perm(f[x], 0, 0x3120), w1 = __byte_perm(f[x + 2], 0, 0x3120);
-                            a0 = e4m3x2_to_f16x2(w0);
-                            a1 = e4m3x2_to_f16x2(w0 >> 16);
-                            a2 = e4m3x2_to_f16x2(w1);
-                            a3 = e4m3x2_to_f16x2(w1 >> 16);
+                            e4m3x4_to_f16x4(__byte_perm(f[x], 0, 0x3120), a0, a1);
+                            e4m3x4_to_f16x4(__byte_perm(f[x + 2], 0, 0x3120), a2, a3);
                         }
 #pragma unroll
                         for (int r = 0; r < NT; ++r)
@@ -580,202 +678,210 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
             }
         }
 
-        if (flags & kLast) {
-            const bool ends = flags & kEnds, whole = begins && ends;
-            const float vs = F8 ? p.v_scale[u / p.hblocks] : 1.f;
-            const int slot = 2 * worker + (begins ? 1 : 0);
+        if constexpr (!WHOLE) {
+            if (flags & kLast) {
+                const int n = tile.x, u = tile.y;
+                const bool ends = flags & kEnds, whole = begins && ends;
+                const float vs = F8 ? p.v_scale[u / p.hblocks] : 1.f;
+                const int slot = 2 * worker + (begins ? 1 : 0);
 #pragma unroll
-            for (int r = 0; r < NT; ++r) {
-                const int h = g + 8 * r;
-                float l = sum[r];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
-                float mul = vs;
-                if (whole) {
-                    const float top = fmaxf(mx[r], sink[r]);
-                    const float f = weight(mx[r], top);
-                    const float tot = top == -INFINITY ? 0.f : l * f + weight(sink[r], top);
-                    mul = tot == 0.f ? 0.f : vs * f / tot;
-                    if (t == 0 && h < heads) {
-                        const int64_t at = int64_t(n) * p.Hq + head0 + h;
-                        p.lse[at] = lse_of(mx[r], top, tot, p.sink, at);
+                for (int r = 0; r < NT; ++r) {
+                    const int h = g + 8 * r;
+                    float l = sum[r];
+                    l += __shfl_xor_sync(0xffffffffu, l, 1);
+                    l += __shfl_xor_sync(0xffffffffu, l, 2);
+                    float mul = vs;
+                    if (whole) {
+                        const float top = fmaxf(mx[r], qa.sink[r]);
+                        const float f = weight(mx[r], top);
+                        const float tot = top == -INFINITY ? 0.f : l * f + weight(qa.sink[r], top);
+                        mul = tot == 0.f ? 0.f : vs * f / tot;
+                        if (t == 0 && h < heads) {
+                            const int64_t at = int64_t(n) * p.Hq + head0 + h;
+                            p.lse[at] = lse_of(mx[r], top, tot, p.sink, at);
+                        }
+                    } else if (t == 0 && h < heads) {
+                        p.part_ml[int64_t(slot) * p.unit_heads + h] = make_float2(mx[r], l);
                     }
-                } else if (t == 0 && h < heads) {
-                    p.part_ml[int64_t(slot) * p.unit_heads + h] = make_float2(mx[r], l);
-                }
-                float* const to = whole ? p.out + (int64_t(n) * p.Hq + head0 + 8 * r) * D
-                                        : p.part_o + (int64_t(slot) * p.unit_heads + 8 * r) * D;
+                    float* const to = whole ? p.out + (int64_t(n) * p.Hq + head0 + 8 * r) * D
+                                            : p.part_o + (int64_t(slot) * p.unit_heads + 8 * r) * D;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float f = __shfl_sync(0xffffffffu, mul, 8 * t + 4 * e);
-                    const int hc = 2 * t + e;  // this thread's O columns
-                    if (8 * r + hc >= heads) continue;
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = __shfl_sync(0xffffffffu, mul, 8 * t + 4 * e);
+                        const int hc = 2 * t + e;  // this thread's O columns
+                        if (8 * r + hc >= heads) continue;
 #pragma unroll
-                    for (int m = 0; m < D / 16; ++m) {
-                        if constexpr (F8) {
-                            *reinterpret_cast<float2*>(to + hc * D + 16 * m + 2 * g) =
-                                make_float2(o[m][r][e] * f, o[m][r][2 + e] * f);
-                        } else {
-                            to[hc * D + 16 * m + g] = o[m][r][e] * f;
-                            to[hc * D + 16 * m + g + 8] = o[m][r][2 + e] * f;
+                        for (int m = 0; m < D / 16; ++m) {
+                            if constexpr (F8) {
+                                *reinterpret_cast<float2*>(to + hc * D + 16 * m + 2 * g) =
+                                    make_float2(o[m][r][e] * f, o[m][r][2 + e] * f);
+                            } else {
+                                to[hc * D + 16 * m + g] = o[m][r][e] * f;
+                                to[hc * D + 16 * m + g + 8] = o[m][r][2 + e] * f;
+                            }
                         }
                     }
                 }
-            }
-            if (begins && !ends) {
-                // the worker of the unit's last tile, which is tiles - 1 - t behind this one
-                const Span sp = span_of<KT>(p, tile.w);
-                const long long rest = sp.tiles - 1 - (tile.z - sp.lo) / KT;
-                rec = Rec{n, u, int(((first + i + rest + 1) * workers - 1) / all) - worker, 0};
+                if (begins && !ends) {
+                    // the worker of the unit's last tile, which is tiles - 1 - t behind this one
+                    const Span sp = span_of<KT>(p, tile.w);
+                    const long long rest = sp.tiles - 1 - (tile.z - sp.lo) / KT;
+                    rec = Rec{int64_t(n) * p.Hq + head0, heads,
+                              int(((first + info.z + rest + 1) * workers - 1) / all) - worker};
+                }
             }
         }
     }
-    if (lane == 0) p.rec[worker] = rec;
+
+    if constexpr (!WHOLE) {
+        if (lane == 0) p.rec[worker] = rec;
+    } else {
+        // ---- join the four warps through their rings, which are free now
+        cp_async_wait_group<0>();
+        const int n = blockIdx.x / units, u = blockIdx.x - n * units;
+#pragma unroll
+        for (int r = 0; r < NT; ++r) {
+            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+            if (t == 0) s_ml[warp][g + 8 * r] = make_float2(mx[r], sum[r]);
+        }
+        __syncwarp();
+        float* const mine = reinterpret_cast<float*>(smem + warp * S::RING);
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+            for (int r = 0; r < NT; ++r)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int h = 8 * r + 2 * t + (e & 1);
+                    const int d = F8 ? 16 * m + 2 * g + (e >> 1) : 16 * m + g + 8 * (e >> 1);
+                    mine[h * S::OROW + d] = o[m][r][e];
+                }
+        __syncthreads();
+        const float vs = F8 ? p.v_scale[u / p.hblocks] : 1.f;
+        for (int it = tid; it < heads * (D / 4); it += kThreads) {
+            const int h = it / (D / 4), d = (it - h * (D / 4)) * 4;
+            const int64_t at = int64_t(n) * p.Hq + head0 + h;
+            const float sk = p.sink ? p.sink[at] * kLog2e : -INFINITY;
+            float2 ml[kWarps];
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                ml[w] = s_ml[w][h];
+                m = fmaxf(m, ml[w].x);
+            }
+            const float top = fmaxf(m, sk);
+            float l = top == -INFINITY ? 0.f : weight(sk, top);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = weight(ml[w].x, top);
+                const float4 x = *reinterpret_cast<const float4*>(smem + w * S::RING + (h * S::OROW + d) * 4);
+                l = fmaf(ml[w].y, f, l);
+                acc.x = fmaf(x.x, f, acc.x);
+                acc.y = fmaf(x.y, f, acc.y);
+                acc.z = fmaf(x.z, f, acc.z);
+                acc.w = fmaf(x.w, f, acc.w);
+            }
+            const float mul = l == 0.f ? 0.f : vs / l;
+            *reinterpret_cast<float4*>(p.out + at * D + d) =
+                make_float4(acc.x * mul, acc.y * mul, acc.z * mul, acc.w * mul);
+            if (d == 0) p.lse[at] = lse_of(m, top, l, p.sink, at);
+        }
+    }
 }
 
 // Joins the parts of each unit that the even split of the tiles cut. Its parts are the
 // second slot of the worker that began it and the first slots of the next `more` workers,
-// in the order of the keys. Every block lists the cut units from the workers' records; a
-// task is one query head of one of them, and as many warps as there are for each (a power
-// of two, up to a block) share its parts: few long units keep the device as busy as many
-// short ones. Each warp adds its parts in order, then one adds the warps' in order.
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams p, int workers,
-                                                                   int block_heads) {
-    constexpr int V = D / 32;  // values of a lane
-    __shared__ int s_owner[kMaxWorkers];
-    __shared__ int s_count[kJoinThreads / 32];
-    __shared__ float s_part[kJoinThreads / 32][D + 2];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// in the order of the keys; blockIdx.y is the query head of the unit. All latency, of loads
+// and of the code itself, which is never in the caches: so two short kernels.
+// CHAINS == false: a warp for each worker's record takes all parts, 16 bytes to a lane.
+// CHAINS (few units, each with many parts): a block for 32 workers' records and
+// blockIdx.z's 32 columns; the warps' quarters take the parts in turn, whole 128-byte lines
+// each, and join by shuffles and through shared memory.
+template <int D, bool CHAINS>
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams p,
+                                                                   int workers) {
     constexpr int WARPS = kJoinThreads / 32;
-    constexpr int PER = (kMaxWorkers + kJoinThreads - 1) / kJoinThreads;
+    constexpr int LANES = CHAINS ? 8 : D / 4;      // that hold a part's columns
+    constexpr int GROUPS = CHAINS ? 4 * WARPS : 32 / LANES;  // parts at a time
+    __shared__ float4 s_acc[WARPS][8];
+    __shared__ float2 s_ml[WARPS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
+    const int w0 = CHAINS ? blockIdx.x * 32 : blockIdx.x * WARPS + warp;
+    const int group = (CHAINS ? warp * 4 : 0) + lane / LANES;
+    const int d = (CHAINS ? blockIdx.z * 32 : 0) + lane % LANES * 4;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    bool cut[PER];
-    int mine = 0;
+    int4 rec = make_int4(0, 0, 0, 0);
+    if (w0 + (CHAINS ? lane : 0) < workers)
+        rec = *reinterpret_cast<const int4*>(p.rec + w0 + (CHAINS ? lane : 0));
+    uint32_t owners = __ballot_sync(0xffffffffu, rec.w > 0 && h < rec.z) & (CHAINS ? 0xffffffffu : 1u);
+    for (; owners != 0; owners &= owners - 1) {
+        const int src = __ffs(owners) - 1;
+        const int64_t row = (int64_t(__shfl_sync(0xffffffffu, rec.y, src)) << 32) +
+                            uint32_t(__shfl_sync(0xffffffffu, rec.x, src)) + h;
+        const int parts = __shfl_sync(0xffffffffu, rec.w, src) + 1;
+        const float sk = p.sink ? p.sink[row] * kLog2e : -INFINITY;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float m = -INFINITY, l = 0.f;
+        for (int x0 = group; x0 < parts; x0 += kJoinBatch * GROUPS) {
+            float2 ml[kJoinBatch];
+            float4 y[kJoinBatch];
 #pragma unroll
-    for (int x = 0; x < PER; ++x) {
-        const int w = tid * PER + x;
-        cut[x] = w < workers && p.rec[w].more > 0;
-        mine += cut[x];
-    }
-    int inc = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += x;
-    }
-    if (lane == 31) s_count[warp] = inc;
-    __syncthreads();
-    int at = inc - mine, owners = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        const int c = s_count[w];
-        if (w < warp) at += c;
-        owners += c;
-    }
-#pragma unroll
-    for (int x = 0; x < PER; ++x)
-        if (cut[x]) s_owner[at++] = tid * PER + x;
-    __syncthreads();
-
-    const int tasks = owners * p.unit_heads;
-    if (tasks == 0) return;
-    int share = 1;  // warps of a task
-    while (share < WARPS && share * 2 * tasks <= int(gridDim.x) * WARPS) share *= 2;
-    const int per_block = WARPS / share, rank = warp % share;
-    for (int base = blockIdx.x * per_block; base < tasks; base += gridDim.x * per_block) {
-        const int task = base + warp / share;
-        float acc[V], m = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = 0.f;
-        int64_t row = -1;
-        if (task < tasks) {
-            const int owner = s_owner[task / p.unit_heads], h = task % p.unit_heads;
-            const Rec rec = p.rec[owner];
-            const int kvh = rec.u / p.hblocks, hb = rec.u - kvh * p.hblocks;
-            if (hb * block_heads + h < p.group) {
-                row = int64_t(rec.n) * p.Hq + kvh * p.group + hb * block_heads + h;
-                const int parts = rec.more + 1, per = (parts + share - 1) / share;
-                const int end = min(parts, (rank + 1) * per);
-                auto slot = [&](int x) {
-                    return int64_t(x == 0 ? 2 * owner + 1 : 2 * (owner + x)) * p.unit_heads + h;
-                };
-                for (int x0 = rank * per; x0 < end; x0 += 32) {  // 32 parts' weights at a time
-                    const float2 ml = x0 + lane < end ? p.part_ml[slot(x0 + lane)] : make_float2(-INFINITY, 0.f);
-                    float top = ml.x;
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    top = fmaxf(top, m);
-                    const float f = weight(m, top);
-                    float w = weight(ml.x, top);
-                    if (ml.x == -INFINITY) w = 0.f;
-                    m = top;
-                    l *= f;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) acc[e] *= f;
-                    float ls = ml.y * w;
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
-                    l += ls;
-                    const int here = min(32, end - x0);
-#pragma unroll 8
-                    for (int x = 0; x < here; ++x) {
-                        const float wx = __shfl_sync(0xffffffffu, w, x);
-                        const float* src = p.part_o + slot(x0 + x) * D + lane * V;
-                        if constexpr (V == 4) {
-                            const float4 y = *reinterpret_cast<const float4*>(src);
-                            acc[0] = fmaf(y.x, wx, acc[0]);
-                            acc[1] = fmaf(y.y, wx, acc[1]);
-                            acc[2] = fmaf(y.z, wx, acc[2]);
-                            acc[3] = fmaf(y.w, wx, acc[3]);
-                        } else {
-                            const float2 y = *reinterpret_cast<const float2*>(src);
-                            acc[0] = fmaf(y.x, wx, acc[0]);
-                            acc[1] = fmaf(y.y, wx, acc[1]);
-                        }
-                    }
+            for (int k = 0; k < kJoinBatch; ++k) {
+                const int x = x0 + k * GROUPS;
+                ml[k] = make_float2(-INFINITY, 0.f);
+                y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (x < parts) {
+                    const int64_t at = int64_t(2 * (w0 + src + x) + (x == 0 ? 1 : 0)) * p.unit_heads + h;
+                    ml[k] = p.part_ml[at];
+                    y[k] = *reinterpret_cast<const float4*>(p.part_o + at * D + d);
                 }
             }
-        }
-        if (share > 1) {
-            __syncthreads();
+            float top = m;
 #pragma unroll
-            for (int e = 0; e < V; ++e) s_part[warp][lane * V + e] = acc[e];
-            if (lane == 0) {
-                s_part[warp][D] = m;
-                s_part[warp][D + 1] = l;
-            }
-            __syncthreads();
-            if (rank == 0) {
-                float top = m;
-                for (int x = 1; x < share; ++x) top = fmaxf(top, s_part[warp + x][D]);
-                const float f = weight(m, top);
-                l *= f;
-#pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] *= f;
-                for (int x = 1; x < share; ++x) {
-                    const float w = weight(s_part[warp + x][D], top);
-                    l = fmaf(s_part[warp + x][D + 1], w, l);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) acc[e] = fmaf(s_part[warp + x][lane * V + e], w, acc[e]);
-                }
-                m = top;
-            }
-        }
-        if (rank == 0 && row >= 0) {
-            const float sk = p.sink ? p.sink[row] * kLog2e : -INFINITY;
-            const float top = fmaxf(m, sk);
+            for (int k = 0; k < kJoinBatch; ++k) top = fmaxf(top, ml[k].x);
             const float f = weight(m, top);
-            const float tot = top == -INFINITY ? 0.f : l * f + weight(sk, top);
-            const float mul = tot == 0.f ? 0.f : f / tot;
+            m = top;
+            l *= f;
+            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] *= mul;
-            float* to = p.out + row * D + lane * V;
-            if constexpr (V == 4) *reinterpret_cast<float4*>(to) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            else *reinterpret_cast<float2*>(to) = make_float2(acc[0], acc[1]);
-            if (lane == 0) p.lse[row] = lse_of(m, top, tot, p.sink, row);
+            for (int k = 0; k < kJoinBatch; ++k) {
+                const float w = weight(ml[k].x, top);
+                l = fmaf(ml[k].y, w, l);
+                acc = make_float4(fmaf(y[k].x, w, acc.x), fmaf(y[k].y, w, acc.y), fmaf(y[k].z, w, acc.z),
+                                  fmaf(y[k].w, w, acc.w));
+            }
         }
+        auto take = [&](const float2& ml, const float4& y) {  // another group's result
+            const float top = fmaxf(m, ml.x), f = weight(m, top), w = weight(ml.x, top);
+            m = top;
+            l = l * f + ml.y * w;
+            acc = make_float4(acc.x * f + y.x * w, acc.y * f + y.y * w, acc.z * f + y.z * w, acc.w * f + y.w * w);
+        };
+#pragma unroll
+        for (int o = LANES; o < 32; o <<= 1)
+            take(make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o)),
+                 make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
+                             __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o)));
+        if constexpr (CHAINS) {
+            __syncthreads();
+            if (lane < LANES) s_acc[warp][lane] = acc;
+            if (lane == 0) s_ml[warp] = make_float2(m, l);
+            __syncthreads();
+            if (warp != 0) continue;
+#pragma unroll 1
+            for (int x = 1; x < WARPS; ++x) take(s_ml[x], s_acc[x][lane % LANES]);
+        }
+        if (lane >= LANES) continue;
+        const float top = fmaxf(m, sk);
+        const float f = weight(m, top);
+        const float tot = top == -INFINITY ? 0.f : l * f + weight(sk, top);
+        const float mul = tot == 0.f ? 0.f : f / tot;
+        *reinterpret_cast<float4*>(p.out + row * D + d) =
+            make_float4(acc.x * mul, acc.y * mul, acc.z * mul, acc.w * mul);
+        if (d == 0) p.lse[row] = lse_of(m, top, tot, p.sink, row);
     }
 }
 
@@ -822,21 +928,32 @@ cudaError_t launch_decode(DecodeParams& p, cudaStream_t st) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decode_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
     // at most the tiles of a full table
     const int span = p.W > 0 && p.W < p.cap ? p.W : p.cap;
     const int64_t unit_tiles = (span + S::KT - 1) / S::KT;
-    const int64_t workers = (int64_t(p.N) * p.Hkv * p.hblocks * unit_tiles + kMinTiles - 1) / kMinTiles;
+    const int64_t units = int64_t(p.N) * p.Hkv * p.hblocks;
+    if (unit_tiles <= kWholeTiles && units <= kWholeUnits) {
+        e = cudaFuncSetAttribute(decode_kernel<S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e != cudaSuccess) return e;
+        decode_kernel<S, true><<<unsigned(units), kThreads, S::SMEM, st>>>(p);
+        return cudaGetLastError();
+    }
+    e = cudaFuncSetAttribute(decode_kernel<S, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t workers = std::max<int64_t>(units * (unit_tiles + 1) / S::MIN_TILES, 1);
     int64_t grid = int64_t(sms) * kCtasPerSm;
     if (grid > kMaxCtas) grid = kMaxCtas;
-    if (grid > workers) grid = workers;
-    decode_kernel<S><<<unsigned(grid), kThreads, S::SMEM, st>>>(p);
+    if (grid > (workers + kWarps - 1) / kWarps) grid = (workers + kWarps - 1) / kWarps;
+    decode_kernel<S, false><<<unsigned(grid), kThreads, S::SMEM, st>>>(p);
     e = cudaGetLastError();
-    if (e != cudaSuccess || unit_tiles == 1) return e;  // units of one tile are never cut
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(sms));
+    // few units make long chains of parts (16 and more at least in the mean)
+    const bool chains = units * 16 <= grid * kWarps;
+    const int window = chains ? 32 : kJoinThreads / 32;
+    cfg.gridDim = dim3(unsigned((grid * kWarps + window - 1) / window), unsigned(p.unit_heads),
+                       chains ? S::D / 32 : 1);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at{};
@@ -844,7 +961,8 @@ cudaError_t launch_decode(DecodeParams& p, cudaStream_t st) {
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_join_kernel<S::D>, DecodeParams(p), int(grid) * kWarps, 8 * S::NT);
+    return cudaLaunchKernelEx(&cfg, chains ? decode_join_kernel<S::D, true> : decode_join_kernel<S::D, false>,
+                              DecodeParams(p), int(grid) * kWarps);
 }
 
 template <int D, bool F8>

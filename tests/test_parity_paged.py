@@ -117,7 +117,7 @@ def check(x, scales, window=0, scale=None, got=None):
     assert np.isfinite(out).all()
     assert (np.abs(out - o_ref) <= o_tol[:, :, None]).all(), float((np.abs(out - o_ref) - o_tol[:, :, None]).max())
     assert np.array_equal(finite, np.isfinite(lse)) and np.array_equal(l_ref[~finite], lse[~finite])
-    assert (np.abs(lse - l_ref)[finite] <= l_tol[finite]).all()
+    assert (np.abs(lse[finite] - l_ref[finite]) <= l_tol[finite]).all()
     return out, lse
 
 
@@ -148,6 +148,31 @@ def test_decode(lens, hq, hkv, d, page, r, window, dtype, layout):
     for n, L in enumerate(lens):
         if L == 0:
             assert not out[n].any() and np.array_equal(lse[n], f64(x["sink"])[n])
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(16, 1, 128, "bf16"), (16, 1, 64, "e4m3"), (4, 2, 128, "e4m3"),
+                                            (40, 2, 64, "bf16")])
+@pytest.mark.parametrize("lens", [[0], [1], [0, 0, 1], [5, 0, 40, 1, 1, 0, 2], [33] * 40])
+def test_decode_short_requests_under_a_long_table(hq, hkv, d, dtype, lens):
+    """The table allows 8192 tokens, so the split form runs, with next to nothing to split."""
+    x, s = problem(lens, hq, hkv, d, 16, 8, dtype, seed=21, max_pages=512)
+    check(x, s)
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(2, 1, 64, "bf16"), (16, 1, 128, "bf16"), (8, 1, 128, "e4m3"),
+                                            (9, 1, 64, "e4m3")])
+def test_decode_one_request_over_all_workers(hq, hkv, d, dtype):
+    """Long chains of parts, joined by whole blocks."""
+    x, s = problem([20011], hq, hkv, d, 64, 256, dtype, seed=22)
+    check(x, s)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_decode_many_units_without_a_split(dtype):
+    """A table of few tiles and more units than CTAs on the device: both sides of the limit of the whole form."""
+    for n in (512, 513):
+        x, s = problem([(7 * i) % 50 for i in range(n)], 4, 2, 64, 16, 8, dtype, seed=n)
+        check(x, s)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
