@@ -8,7 +8,6 @@ missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -483,35 +482,33 @@ def l2clip_backward(x, dy, threshold: float, scale=None, tau=None, stream=None):
 # --------------------------------------------------------------------------
 # serving: paged key-value cache and single-token attention (include/inkling_paged_attn.h)
 # --------------------------------------------------------------------------
-def _on_device(device, **tensors):
-    """ValueError unless every given (tensor, dtype) is contiguous, of that dtype and on `device`."""
-    for name, (t, dtype) in tensors.items():
-        if t is None:
-            continue
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+_bound = None
 
 
-def _shape(name, t, *want):
-    if t is not None and tuple(t.shape) != want:
-        raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+def _serving():
+    """The `_serving` extension (csrc/serving_ext.cpp), calling the loaded library."""
+    global _bound
+    lib = load()
+    from . import _serving as ext
+    if _bound is not lib:
+        ext.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.inkling_kv_plan, lib.inkling_kv_append, lib.inkling_rel_attn_decode,
+            lib.inkling_rel_attn_decode_workspace_size)))
+        _bound = lib
+    return ext
 
 
-def _allocating_on(stream):
-    """Tensors allocated inside belong to `stream` (None: the current one), so that one that is
-    dropped when a call returns is not reused before that stream is done with it."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _current(stream, device):
+    """Makes `stream` current, so that what a call allocates belongs to it as well."""
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
-def _stream_on(device, stream):
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if s.device != device:
-        raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
-    return ctypes.c_void_p(s.cuda_stream)
+def _result(r, where: str):
+    if type(r) is int:
+        raise InklingError(r, where)
+    return r
 
 
 def make_kv_cache_desc(k_cache: torch.Tensor, v_cache: torch.Tensor) -> KVCacheDesc:
@@ -528,21 +525,12 @@ def make_kv_cache_desc(k_cache: torch.Tensor, v_cache: torch.Tensor) -> KVCacheD
     return KVCacheDesc(*k_cache.shape, KV_DTYPES[k_cache.dtype], ks[0], ks[1], ks[2])
 
 
-def _kv_scales(cache: torch.Tensor, k_scale, v_scale):
-    quantised = cache.dtype == torch.float8_e4m3fn
-    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if (s is not None) != quantised:
-            raise ValueError(f"{name}: an e4m3 cache needs its scales, a bfloat16 cache takes none")
-        _shape(name, s, cache.shape[2])
-    _on_device(cache.device, k_scale=(k_scale, torch.float32), v_scale=(v_scale, torch.float32))
-
-
 def inkling_kv_plan(dims: KVPlanDims, old_lens, new_lens, block_table, free_pages, free_count, lens, query_start,
                     slots, positions, info, stream=None) -> None:
     with torch.cuda.device(block_table.device):
         st = load().inkling_kv_plan(
             ctypes.byref(dims), _p(old_lens), _p(new_lens), _p(block_table), _p(free_pages), _p(free_count), _p(lens),
-            _p(query_start), _p(slots), _p(positions), _p(info), _stream_on(block_table.device, stream))
+            _p(query_start), _p(slots), _p(positions), _p(info), _stream(stream))
     _check(st, "inkling_kv_plan")
 
 
@@ -551,7 +539,7 @@ def inkling_kv_append(cache: KVCacheDesc, dims: KVAppendDims, k, v, slots, k_sca
     with torch.cuda.device(k_cache.device):
         st = load().inkling_kv_append(
             ctypes.byref(cache), ctypes.byref(dims), _p(k), _p(v), _p(slots), _p(k_scale), _p(v_scale),
-            _p(clip_scale), _p(tau), _p(k_cache), _p(v_cache), _stream_on(k_cache.device, stream))
+            _p(clip_scale), _p(tau), _p(k_cache), _p(v_cache), _stream(stream))
     _check(st, "inkling_kv_append")
 
 
@@ -572,12 +560,12 @@ def inkling_rel_attn_decode(cache: KVCacheDesc, dims: DecodeDims, q, k_cache, v_
         st = load().inkling_rel_attn_decode(
             ctypes.byref(cache), ctypes.byref(dims), _p(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
             _p(profiles), _p(sink), _p(block_table), _p(lens), _p(out), _p(lse), _p(workspace), workspace.numel(),
-            _stream_on(k_cache.device, stream))
+            _stream(stream))
     _check(st, "inkling_rel_attn_decode")
 
 
 def kv_plan(old_lens, new_lens, block_table, free_pages, free_count, *, page_size: int, num_pages: int,
-            max_tokens: int, stream=None):
+            max_tokens: int, lens=None, info=None, stream=None):
     """Pages and slots of a serving step, from the requests' lengths before and after it.
 
     ``old_lens``, ``new_lens`` [N], ``block_table`` [N, M], ``free_pages`` [num_pages] and
@@ -585,32 +573,15 @@ def kv_plan(old_lens, new_lens, block_table, free_pages, free_count, *, page_siz
     in place. Returns a dict: ``lens`` [N] (tokens that have a page), ``query_start`` [N + 1],
     ``slots`` [max_tokens] int64, ``positions`` [max_tokens] and ``info`` [4] (pages free
     afterwards, new tokens, pages short, pages taken). ``info[:1]`` is the next call's
-    ``free_count`` (see include/inkling_paged_attn.h).
+    ``free_count`` (see include/inkling_paged_attn.h). ``lens`` and ``info`` may be given,
+    to be written; they may not overlap an input.
     """
-    device, i32 = block_table.device, torch.int32
-    if block_table.dim() != 2 or not block_table.is_cuda:
-        raise ValueError("block_table must be a CUDA tensor [requests, max_pages]")
-    N, M = block_table.shape
-    _on_device(device, block_table=(block_table, i32), old_lens=(old_lens, i32), new_lens=(new_lens, i32),
-               free_pages=(free_pages, i32), free_count=(free_count, i32))
-    _shape("old_lens", old_lens, N)
-    _shape("new_lens", new_lens, N)
-    _shape("free_pages", free_pages, int(num_pages))
-    _shape("free_count", free_count, 1)
-    dims = KVPlanDims(N, int(page_size), M, int(num_pages), int(max_tokens))
-    if max_tokens < 0:
-        raise ValueError("max_tokens must not be negative")
-    # one allocation for the four int32 outputs, each at a multiple of 16 bytes
-    up = lambda n: (n + 3) // 4 * 4  # noqa: E731
-    at = [0, up(N), up(N) + up(N + 1), up(N) + up(N + 1) + up(max_tokens)]
-    with _allocating_on(stream):
-        small = torch.empty(at[3] + 4, dtype=i32, device=device)
-        slots = torch.empty(max_tokens, dtype=torch.int64, device=device)
-    lens, query_start = small[:N], small[at[1]:at[1] + N + 1]
-    positions, info = small[at[2]:at[2] + max_tokens], small[at[3]:]
-    inkling_kv_plan(dims, old_lens, new_lens, block_table, free_pages, free_count, lens, query_start, slots, positions,
-                    info, stream)
-    return dict(lens=lens, query_start=query_start, slots=slots, positions=positions, info=info)
+    if stream is not None:
+        with _current(stream, block_table.device):
+            return kv_plan(old_lens, new_lens, block_table, free_pages, free_count, page_size=page_size,
+                           num_pages=num_pages, max_tokens=max_tokens, lens=lens, info=info)
+    return _result(_serving().kv_plan(old_lens, new_lens, block_table, free_pages, free_count, page_size, num_pages,
+                                      max_tokens, lens, info), "inkling_kv_plan")
 
 
 def kv_append(k, v, slots, k_cache, v_cache, *, k_scale=None, v_scale=None, threshold: Optional[float] = None,
@@ -621,28 +592,12 @@ def kv_append(k, v, slots, k_cache, v_cache, *, k_scale=None, v_scale=None, thre
     values dense). With a ``threshold``, k goes through L2Clip (``clip_scale`` [Hkv, D],
     ``tau`` [T]) on the way; an e4m3 cache takes ``k_scale``, ``v_scale`` [Hkv].
     """
-    desc = make_kv_cache_desc(k_cache, v_cache)
-    device = k_cache.device
-    _, _, H, D = k_cache.shape
-    T = slots.numel()
-    for name, x in (("k", k), ("v", v)):
-        _shape(name, x, T, H, D)
-        if x.device != device or x.dtype != torch.bfloat16:
-            raise ValueError(f"{name} must be bfloat16 on {device}")
-        s = x.stride()
-        if T > 0 and ((D > 1 and s[2] != 1) or (H > 1 and s[1] != D)):
-            raise ValueError(f"{name} must have dense heads and values")
-    _shape("slots", slots, T)
-    _on_device(device, slots=(slots, torch.int64), clip_scale=(clip_scale, torch.float32), tau=(tau, torch.float32))
-    _shape("clip_scale", clip_scale, H, D)
-    _shape("tau", tau, T)
-    _kv_scales(k_cache, k_scale, v_scale)
-    if threshold is None and (clip_scale is not None or tau is not None):
-        raise ValueError("clip_scale and tau need a threshold")
-    one = H * D  # the stride of a single row means nothing
-    dims = KVAppendDims(T, k.stride(0) if T > 1 else one, v.stride(0) if T > 1 else one, int(threshold is not None),
-                        0.0 if threshold is None else float(threshold))
-    inkling_kv_append(desc, dims, k, v, slots, k_scale, v_scale, clip_scale, tau, k_cache, v_cache, stream)
+    if stream is not None:
+        with _current(stream, k_cache.device):
+            return kv_append(k, v, slots, k_cache, v_cache, k_scale=k_scale, v_scale=v_scale, threshold=threshold,
+                             clip_scale=clip_scale, tau=tau)
+    return _result(_serving().kv_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, threshold, clip_scale, tau),
+                   "inkling_kv_append")
 
 
 def paged_decode(q, k_cache, v_cache, block_table, lens, profiles=None, sink=None, *, window: int = 0,
@@ -652,36 +607,12 @@ def paged_decode(q, k_cache, v_cache, block_table, lens, profiles=None, sink=Non
     ``q`` [N,Hq,D] BF16, pools [num_pages, page_size, Hkv, D] BF16 or e4m3 (then with
     ``k_scale``, ``v_scale`` [Hkv]), ``block_table`` [N,M] int32, ``lens`` [N] int32 with the
     new token counted (0: a padding row), ``profiles`` [N,Hq,R] BF16, ``sink`` [N,Hq] fp32
-    (see include/inkling_paged_attn.h).
+    (see include/inkling_paged_attn.h). ``workspace``: ``alloc_decode_workspace``'s, for a
+    caller that keeps one.
     """
-    desc = make_kv_cache_desc(k_cache, v_cache)
-    device = k_cache.device
-    if q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
-        raise ValueError("q must be [requests, heads_q, head_dim] with the cache's head_dim")
-    N, Hq, D = q.shape
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [requests, max_pages]")
-    M = block_table.shape[1]
-    R = 0
-    if profiles is not None:
-        if profiles.dim() != 3:
-            raise ValueError("profiles must be [requests, heads_q, rel_extent]")
-        R = profiles.shape[2]
-        _shape("profiles", profiles, N, Hq, R)
-    _shape("block_table", block_table, N, M)
-    _shape("lens", lens, N)
-    _shape("sink", sink, N, Hq)
-    _on_device(device, q=(q, torch.bfloat16), block_table=(block_table, torch.int32), lens=(lens, torch.int32),
-               profiles=(profiles, torch.bfloat16), sink=(sink, torch.float32),
-               workspace=(workspace, torch.uint8))
-    _kv_scales(k_cache, k_scale, v_scale)
-    dims = DecodeDims(N, Hq, R, int(window), M, 0.0 if scale is None else float(scale))
-    with _allocating_on(stream):
-        if workspace is None:
-            n = inkling_rel_attn_decode_workspace_size(desc, dims)
-            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=device)
-        out = torch.empty(q.shape, dtype=torch.float32, device=device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=device)
-    inkling_rel_attn_decode(desc, dims, q, k_cache, v_cache, k_scale, v_scale, profiles if R else None, sink,
-                            block_table, lens, out, lse, workspace, stream)
-    return out, lse
+    if stream is not None:
+        with _current(stream, k_cache.device):
+            return paged_decode(q, k_cache, v_cache, block_table, lens, profiles, sink, window=window, scale=scale,
+                                k_scale=k_scale, v_scale=v_scale, workspace=workspace)
+    return _result(_serving().paged_decode(q, k_cache, v_cache, block_table, lens, profiles, sink, window, scale,
+                                           k_scale, v_scale, workspace), "inkling_rel_attn_decode")

@@ -1,4 +1,5 @@
-"""Build libinkling_rel_attn.so in-tree with nvcc for sm_100a.
+"""Build libinkling_rel_attn.so in-tree with nvcc for sm_100a, and the Python module
+``_serving`` (csrc/serving_ext.cpp) with the host compiler against PyTorch.
 
 Usage: ``python -m learned_relative_gqa_b200.build [--verbose]``.
 The library is written next to this file; nothing is installed elsewhere.
@@ -17,6 +18,9 @@ LIB_NAME = "libinkling_rel_attn.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 # the same kernels with every shared / global index checked (-DINKLING_BOUNDS_CHECK), for tests
 BOUNDS_CHECK_LIB_PATH = os.path.join(HERE, "libinkling_rel_attn_boundscheck.so")
+# the serving calls on PyTorch tensors; it takes the library's entry points when that is loaded
+EXT_SOURCE = os.path.join(CSRC, "serving_ext.cpp")
+EXT_PATH = os.path.join(HERE, "_serving.so")
 SOURCES = ["host.cu", "prep_kernels.cu", "fwd.cu", "bwd.cu", "l2clip.cu", "paged_cache.cu", "decode.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -40,10 +44,26 @@ def stale(path: str = LIB_PATH) -> bool:
 _stale = stale
 
 
+def ext_command(out_path: str) -> list:
+    """The host compiler's command line for the Python module."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda", "include")
+    include = [INCLUDE, sysconfig.get_paths()["include"], cuda]
+    torch_include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include")]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", EXT_SOURCE, "-o", out_path]
+            + [f"-I{d}" for d in include] + [a for d in torch_include for a in ("-isystem", d)]
+            + [f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+
+
 def build(force: bool = False, verbose: bool = False, out_path: str = LIB_PATH, defines: tuple = ()) -> str:
     """Compile the library. ``defines`` / ``out_path`` build diagnostic variants
     (for example ``INKLING_TRACE``) next to, not over, the product library."""
-    if not force and not defines and out_path == LIB_PATH and not _stale():
+    if not force and not defines and out_path == LIB_PATH and not _stale() and not stale(EXT_PATH):
         return LIB_PATH
     objs = []
     build_dir = os.path.join(ROOT, "_build", "-".join(defines) or "default")
@@ -58,9 +78,14 @@ def build(force: bool = False, verbose: bool = False, out_path: str = LIB_PATH, 
         obj = os.path.join(build_dir, src.replace(".cu", ".o"))
         procs.append((subprocess.Popen(common + ["-c", os.path.join(CSRC, src), "-o", obj]), src))
         objs.append(obj)
+    product = out_path == LIB_PATH and not defines
+    if product:
+        procs.append((subprocess.Popen(ext_command(EXT_PATH + ".tmp")), os.path.basename(EXT_SOURCE)))
     failed = [src for proc, src in procs if proc.wait() != 0]
     if failed:
-        raise RuntimeError(f"nvcc failed on {', '.join(failed)}")
+        raise RuntimeError(f"the compiler failed on {', '.join(failed)}")
+    if product:
+        os.replace(EXT_PATH + ".tmp", EXT_PATH)
     tmp = out_path + ".tmp"
     subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, out_path)

@@ -44,7 +44,9 @@ class PagedKVCache:
         self.k_cache = torch.zeros(pool, dtype=dtype, device=device).transpose(1, 2)
         self.v_cache = torch.zeros(pool, dtype=dtype, device=device).transpose(1, 2)
         self.k_scale, self.v_scale = k_scale, v_scale
-        binding._kv_scales(self.k_cache, k_scale, v_scale)
+        for name, scale in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if (scale is not None) != (dtype == torch.float8_e4m3fn):
+                raise ValueError(f"PagedKVCache: {name}: an e4m3 cache needs its scales, a bfloat16 cache takes none")
         i32 = dict(dtype=torch.int32, device=device)
         self.block_table = torch.full((max_requests, width), -1, **i32)
         self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)  # page 0 on top
@@ -55,7 +57,7 @@ class PagedKVCache:
         self._state[at] = num_pages
         self._next = torch.zeros_like(self._state)
         self.lens = self._state[:max_requests]
-        self.info = self._state[at:]
+        self.info, self._free_count = self._state[at:], self._state[at:at + 1]
         self._next_lens, self._next_info = self._next[:max_requests], self._next[at:]
 
     def reserve(self, new_lens: torch.Tensor, max_tokens: int, stream=None):
@@ -65,21 +67,15 @@ class PagedKVCache:
         ``cache.lens`` holds the lengths that the free pages allowed and ``cache.info`` the
         pages left, the new tokens, the pages that were missing and the pages taken.
         """
-        N, M = self.block_table.shape
-        device = self.block_table.device
-        binding._on_device(device, new_lens=(new_lens, torch.int32))
-        binding._shape("new_lens", new_lens, N)
-        if max_tokens < 0:
-            raise ValueError("max_tokens must not be negative")
-        with binding._allocating_on(stream):
-            i32 = dict(dtype=torch.int32, device=device)
-            query_start, positions = torch.empty(N + 1, **i32), torch.empty(max_tokens, **i32)
-            slots = torch.empty(max_tokens, dtype=torch.int64, device=device)
-            dims = binding.KVPlanDims(N, self.page_size, M, self.num_pages, int(max_tokens))
-            binding.inkling_kv_plan(dims, self.lens, new_lens, self.block_table, self.free_pages, self.info[:1],
-                                    self._next_lens, query_start, slots, positions, self._next_info, stream)
+        plan = binding.kv_plan(self.lens, new_lens, self.block_table, self.free_pages, self._free_count,
+                               page_size=self.page_size, num_pages=self.num_pages, max_tokens=max_tokens,
+                               lens=self._next_lens, info=self._next_info, stream=stream)
+        if stream is None:
             self._state.copy_(self._next)
-        return dict(slots=slots, positions=positions, query_start=query_start)
+        else:
+            with torch.cuda.stream(stream):
+                self._state.copy_(self._next)
+        return {name: plan[name] for name in ("slots", "positions", "query_start")}
 
     def append(self, k, v, slots, *, threshold: Optional[float] = None, clip_scale=None, tau=None, stream=None) -> None:
         """Stores ``k``, ``v`` [T, heads_kv, head_dim] BF16 in their slots (see ``binding.kv_append``)."""

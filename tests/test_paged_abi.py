@@ -165,16 +165,20 @@ def test_python_wrappers_refuse_wrong_tensors(lib):
     t = torch.zeros(2, 3, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA tensor"):
         binding.kv_plan(t[:, 0], t[:, 0], t, t[0], t[0, :1], page_size=16, num_pages=3, max_tokens=4)
-    with pytest.raises(ValueError, match="expected cuda"):
-        binding._on_device(torch.device("cuda", 0), lens=(t, torch.int32))
-    with pytest.raises(ValueError, match="must be torch.int64"):
-        binding._on_device(t.device, slots=(t, torch.int64))
-    with pytest.raises(ValueError, match="contiguous"):
-        binding._on_device(t.device, slots=(t.t(), torch.int32))
-    with pytest.raises(ValueError, match="shape"):
-        binding._shape("lens", t, 3, 2)
-    with pytest.raises(ValueError, match="scales"):
-        binding._kv_scales(k, torch.ones(2), torch.ones(2))
+    with pytest.raises(TypeError, match="old_lens must be a tensor"):
+        binding.kv_plan([1, 2], t[:, 0], t, t[0], t[0, :1], page_size=16, num_pages=3, max_tokens=4)
+    with pytest.raises(TypeError):
+        binding.kv_plan(t[:, 0], t[:, 0], t, t[0], t[0, :1], page_size="16", num_pages=3, max_tokens=4)
+    with pytest.raises(ValueError, match="CUDA device"):
+        binding.kv_append(k[0, :, :1], k[0, :, :1], torch.zeros(16, dtype=torch.int64), k, k)
+    with pytest.raises(ValueError, match="one shape"):
+        binding.kv_append(k[0], k[0], torch.zeros(16, dtype=torch.int64), k, k.float())
+    with pytest.raises(ValueError, match="bfloat16 or"):
+        binding.paged_decode(k[0], k.float(), k.float(), t, t[:, 0])
+    with pytest.raises(ValueError, match="same strides"):
+        binding.paged_decode(k[0], k.clone().transpose(0, 1).contiguous().transpose(0, 1), k, t, t[:, 0])
+    with pytest.raises(TypeError, match="lens must be a tensor"):
+        binding.paged_decode(k[0], k, k, t, None)
     from learned_relative_gqa_b200.paged import PagedKVCache
     with pytest.raises(ValueError, match="positive"):
         PagedKVCache(max_requests=1, max_len=0, num_pages=1, page_size=16, heads_kv=1, head_dim=64, device="cpu")
