@@ -41,7 +41,7 @@ typedef enum {
 
 /*
  * num_pages   pages in each pool (1 .. 2^31 - 1)
- * page_size   tokens in a page, any number from 1 (below 2^30)
+ * page_size   tokens in a page, any number from 1 (below 2^30); num_pages * page_size <= 2^31
  * heads_kv    Hkv
  * head_dim    D: 64 or 128
  * dtype       inkling_kv_dtype

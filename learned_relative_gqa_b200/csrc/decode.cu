@@ -72,8 +72,8 @@ struct alignas(16) Rec {
 };
 
 struct DecodeParams {
-    int N, Hq, Hkv, group, hblocks, unit_heads, R, W, M, P, num_pages, cap;
-    uint32_t p_mul, p_shift;  // j / P = j p_mul >> p_shift
+    int N, Hq, Hkv, group, hblocks, unit_heads, R, W, M, num_pages, cap;
+    PageDivisor page;
     int64_t page_stride, token_stride, head_stride;  // bytes
     float scale_log2;
     const uint16_t* q;
@@ -179,10 +179,6 @@ __device__ __forceinline__ Span span_of(const DecodeParams& p, int raw_len) {
     s.lo = p.W > 0 ? max(s.len - p.W, 0) : 0;
     s.tiles = max((s.len - s.lo + KT - 1) / KT, 1);
     return s;
-}
-
-__device__ __forceinline__ int page_index(const DecodeParams& p, int j) {
-    return int((uint64_t(uint32_t(j)) * p.p_mul) >> p.p_shift);
 }
 
 // lse of a row from the maximum of its keys' logits, that of those and the sink (log2 units),
@@ -316,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     };
     auto lookup = [&](const Cursor& c) {  // -1: not allowed
         const int j = c.s.lo + c.t * KT + my_key;
-        return j < c.s.len ? p.table[int64_t(c.n) * p.M + page_index(p, j)] : -1;
+        return j < c.s.len ? p.table[int64_t(c.n) * p.M + p.page.index(j)] : -1;
     };
     auto issue = [&](const Cursor& c, int i, int stage, int page) {
         const int j0 = c.s.lo + c.t * KT, j = j0 + my_key;
@@ -333,11 +329,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
                                              c.at, 0);
         }
         const uint32_t dst = ring + stage * S::STAGE;
-        const int offset = j - page_index(p, j) * p.P;  // in its page
+        const int offset = j - p.page.index(j) * p.page.size;  // in its page
         int64_t at = ok ? int64_t(page) * p.page_stride + int64_t(offset) * p.token_stride + kvh * p.head_stride : 0;
         constexpr int ROWS = 32 / S::CPR;  // of a copy of 16 bytes per lane
         const int r0 = lane / S::CPR, ch = lane % S::CPR;
-        if (mask == kAll && __shfl_sync(0xffffffffu, offset, 0) + KT <= p.P) {
+        if (mask == kAll && __shfl_sync(0xffffffffu, offset, 0) + KT <= p.page.size) {
             // the usual tile: every key allowed, all in one page, so rows follow each other
             at = __shfl_sync(0xffffffffu, at, 0) + r0 * p.token_stride + ch * 16;
             const uint8_t *k = p.k_cache + at, *v = p.v_cache + at;
@@ -1013,15 +1009,9 @@ inkling_status inkling_rel_attn_decode(const inkling_kv_cache_desc* cache, const
     p.R = int(dims->rel_extent);
     p.W = int(dims->window);
     p.M = int(dims->max_pages);
-    p.P = int(cache->page_size);
+    p.page = PageDivisor(cache->page_size);
     p.num_pages = int(cache->num_pages);
     p.cap = int(dims->max_pages * cache->page_size);
-    // j / P for j < 2^31 by a multiplication (Granlund and Montgomery): with 2^s >= P and
-    // m = floor(2^(31+s) / P) + 1, m P - 2^(31+s) <= 2^s, so j m >> (31 + s) is exact
-    uint32_t shift = 0;
-    while ((int64_t(1) << shift) < p.P) ++shift;
-    p.p_mul = uint32_t((uint64_t(1) << (31 + shift)) / uint64_t(p.P) + 1);
-    p.p_shift = 31 + shift;
     const int64_t es = lay.e4m3 ? 1 : 2;
     p.page_stride = lay.page_stride * es;
     p.token_stride = lay.token_stride * es;

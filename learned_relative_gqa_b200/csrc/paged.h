@@ -19,6 +19,23 @@ struct CacheLayout {
 };
 inkling_status check_cache(const inkling_kv_cache_desc* c, CacheLayout* out);
 
+// j / size for 0 <= j < 2^31 by a multiplication (Granlund and Montgomery): with 2^s >= size
+// and m = floor(2^(31+s) / size) + 1, m size - 2^(31+s) <= 2^s, so j m >> (31 + s) is exact.
+struct PageDivisor {
+    int size = 1;
+    uint32_t mul = 0, shift = 0;
+    PageDivisor() = default;
+    explicit PageDivisor(int64_t page_size) : size(int(page_size)) {
+        uint32_t s = 0;
+        while ((int64_t(1) << s) < page_size) ++s;
+        mul = uint32_t((uint64_t(1) << (31 + s)) / uint64_t(page_size) + 1);
+        shift = 31 + s;
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int index(int j) const { return int((uint64_t(uint32_t(j)) * mul) >> shift); }
+#endif
+};
+
 inline bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 // A named NVTX range over an entry point (a no-op when no profiler is attached).

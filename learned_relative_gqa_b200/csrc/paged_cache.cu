@@ -20,7 +20,8 @@ using namespace ira;
 // inkling_kv_plan
 // --------------------------------------------------------------------------
 struct PlanParams {
-    int N, P, M, num_pages, T;
+    int N, M, num_pages, T;
+    PageDivisor page;
     const int32_t* old_lens;
     const int32_t* new_lens;
     int32_t* table;
@@ -33,9 +34,11 @@ struct PlanParams {
     int32_t* info;
 };
 
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 1024;
 
-__device__ __forceinline__ int pages_of(int len, int P) { return len > 0 ? (len - 1) / P + 1 : 0; }
+__device__ __forceinline__ int pages_of(int len, const PageDivisor& page) {
+    return len > 0 ? page.index(len - 1) + 1 : 0;
+}
 
 // Largest r in [0, n) with at[r] <= x, for a non-decreasing at with at[0] = 0 <= x.
 __device__ __forceinline__ int last_at_or_below(const int* at, int n, int x) {
@@ -49,29 +52,33 @@ __device__ __forceinline__ int last_at_or_below(const int* at, int n, int x) {
 }
 
 // The plan is three prefix sums over the requests (new tokens, pages to take, pages to
-// give back) and then independent writes: token i, taken page k and returned page i each
-// find their request by bisection. Bound by launch and load latency (a few microseconds
-// of work), so it is one kernel with no exchange between blocks: every block computes all
-// three sums itself (N <= 16384 lengths, from L2 after the first block) into shared memory
-// and takes its share of the writes. The stack needs no order between blocks either: a
-// page popped in the same call that returned it is read from the block table, so no block
-// reads an entry of free_pages or of the table that another one writes.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
+// give back) and then independent writes: each new token, taken page, returned page and
+// request is an item of its own, and finds its request by bisection. Bound by launch and
+// load latency (a few microseconds of work), so it is one kernel with no exchange between
+// blocks, all items side by side: every block computes the three sums itself (N <= 16384
+// lengths, from L2 after the first block) into shared memory and takes its share of the
+// items. The stack needs no order between blocks either: a page popped in the same call that
+// returned it is read from the block table, so no block reads an entry of free_pages or of
+// the table that another one writes. The code is kept short: it is as cold as the data.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanParams p) {
     extern __shared__ int s_at[];
     int* s_tok = s_at;               // [N + 1] exclusive prefix sums, totals at [N]
     int* s_need = s_tok + p.N + 1;
     int* s_back = s_need + p.N + 1;
-    __shared__ int3 s_warp[kPlanThreads / 32];
+    __shared__ int3 s_warp[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int cap = p.M * p.P;
-    auto clamped = [&](int len) { return min(max(len, 0), cap); };
+    const int free_count = __ldg(p.free_count);
+    const int cap = p.M * p.page.size;
+    auto old_len = [&](int r) { return min(max(__ldg(p.old_lens + r), 0), cap); };
+    auto new_len = [&](int r) { return min(max(__ldg(p.new_lens + r), 0), cap); };
 
     const int chunk = (p.N + kPlanThreads - 1) / kPlanThreads;
     const int r0 = min(tid * chunk, p.N), r1 = min(r0 + chunk, p.N);
     int3 sum = make_int3(0, 0, 0);
+#pragma unroll 4
     for (int r = r0; r < r1; ++r) {
-        const int o = clamped(p.old_lens[r]), w = clamped(p.new_lens[r]);
-        const int held = pages_of(o, p.P), want = pages_of(w, p.P);
+        const int o = old_len(r), w = new_len(r);
+        const int held = pages_of(o, p.page), want = pages_of(w, p.page);
         s_tok[r] = sum.x;
         s_need[r] = sum.y;
         s_back[r] = sum.z;
@@ -79,33 +86,26 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
         sum.y += max(want - held, 0);
         sum.z += max(held - want, 0);
     }
-    int3 inc = sum;
+    auto scan = [&](int3 v) {  // inclusive, over the warp
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc.x, d), y = __shfl_up_sync(0xffffffffu, inc.y, d),
-                  z = __shfl_up_sync(0xffffffffu, inc.z, d);
-        if (lane >= d) {
-            inc.x += x;
-            inc.y += y;
-            inc.z += z;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, v.x, d), y = __shfl_up_sync(0xffffffffu, v.y, d),
+                      z = __shfl_up_sync(0xffffffffu, v.z, d);
+            if (lane >= d) v = make_int3(v.x + x, v.y + y, v.z + z);
         }
-    }
+        return v;
+    };
+    const int3 inc = scan(sum);
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
-    int3 ex = make_int3(inc.x - sum.x, inc.y - sum.y, inc.z - sum.z);
-    int3 all = make_int3(0, 0, 0);
-#pragma unroll
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        const int3 v = s_warp[w];
-        if (w < warp) {
-            ex.x += v.x;
-            ex.y += v.y;
-            ex.z += v.z;
-        }
-        all.x += v.x;
-        all.y += v.y;
-        all.z += v.z;
-    }
+    const int3 warps = scan(lane < kPlanThreads / 32 ? s_warp[lane] : make_int3(0, 0, 0));
+    const int3 all = make_int3(__shfl_sync(0xffffffffu, warps.x, 31), __shfl_sync(0xffffffffu, warps.y, 31),
+                               __shfl_sync(0xffffffffu, warps.z, 31));
+    const int prev = max(warp - 1, 0);
+    int3 ex = make_int3(__shfl_sync(0xffffffffu, warps.x, prev), __shfl_sync(0xffffffffu, warps.y, prev),
+                        __shfl_sync(0xffffffffu, warps.z, prev));
+    if (warp == 0) ex = make_int3(0, 0, 0);
+    ex = make_int3(ex.x + inc.x - sum.x, ex.y + inc.y - sum.y, ex.z + inc.z - sum.z);
     for (int r = r0; r < r1; ++r) {
         s_tok[r] += ex.x;
         s_need[r] += ex.y;
@@ -118,66 +118,65 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
     }
     __syncthreads();
 
-    const int count = min(max(*p.free_count, 0), p.num_pages);
+    const int count = min(max(free_count, 0), p.num_pages);
     // returned pages beyond the stack's room (malformed tables only) are dropped
     const int back = min(all.z, p.num_pages - count);
     const int avail = count + back;
     const int taken = min(all.y, avail);
     const int left = avail - taken;
+    const int kept = min(back, max(left - count, 0));  // returned pages that this call does not pop again
 
-    // i-th returned page and k-th taken page
     auto returned = [&](int i) {
         const int r = last_at_or_below(s_back, p.N, i);
-        const int want = pages_of(clamped(p.new_lens[r]), p.P);
-        return p.table[int64_t(r) * p.M + want + (i - s_back[r])];
+        return p.table[int64_t(r) * p.M + pages_of(new_len(r), p.page) + (i - s_back[r])];
     };
     auto popped = [&](int k) {
         const int at = avail - 1 - k;
         return at < count ? p.free_pages[at] : returned(at - count);
     };
 
-    const int gid = blockIdx.x * kPlanThreads + tid, stride = gridDim.x * kPlanThreads;
-    for (int i = gid; i < p.T; i += stride) {
-        int64_t slot = -1;
-        int pos = 0;
-        if (i < all.x) {
-            const int r = last_at_or_below(s_tok, p.N, i);
-            const int o = clamped(p.old_lens[r]);
-            const int held = pages_of(o, p.P);
-            pos = o + (i - s_tok[r]);
-            const int idx = pos / p.P;
-            int page = -1;
-            if (idx < held) {
-                page = p.table[int64_t(r) * p.M + idx];
-            } else {
+    const int64_t items = int64_t(p.T) + taken + kept + p.N + 1;
+    for (int64_t item = int64_t(blockIdx.x) * kPlanThreads + tid; item < items; item += gridDim.x * kPlanThreads) {
+        if (item < int64_t(p.T) + taken) {  // a token, or a page taken
+            const bool token = item < p.T;
+            const int i = int(token ? item : item - p.T);
+            int64_t slot = -1;
+            int pos = 0;
+            if (!token || i < all.x) {
+                const int* at = token ? s_tok : s_need;
+                const int r = last_at_or_below(at, p.N, i);
+                const int o = old_len(r), held = pages_of(o, p.page);
+                pos = o + (i - at[r]);
+                const int idx = token ? p.page.index(pos) : held + (i - at[r]);
                 const int k = s_need[r] + (idx - held);
-                if (k < taken) page = popped(k);
+                int page = -1;
+                if (idx < held) page = p.table[int64_t(r) * p.M + idx];
+                else if (k < taken) page = popped(k);
+                if (!token) p.table[int64_t(r) * p.M + idx] = page;
+                if (page >= 0 && page < p.num_pages) slot = int64_t(page) * p.page.size + (pos - idx * p.page.size);
             }
-            if (page >= 0 && page < p.num_pages) slot = int64_t(page) * p.P + (pos - idx * p.P);
+            if (token) {
+                p.slots[i] = slot;
+                p.positions[i] = pos;
+            }
+        } else if (item < int64_t(p.T) + taken + kept) {
+            const int i = int(item - p.T - taken);
+            p.free_pages[count + i] = returned(i);
+        } else {
+            const int r = int(item - p.T - taken - kept);
+            p.query_start[r] = s_tok[r];
+            if (r == p.N) {
+                p.info[0] = left;
+                p.info[1] = all.x;
+                p.info[2] = all.y - taken;
+                p.info[3] = taken;
+            } else {
+                const int o = old_len(r), w = new_len(r);
+                const int64_t given = min(max(taken - s_need[r], 0), s_need[r + 1] - s_need[r]);
+                const int64_t room = (pages_of(o, p.page) + given) * p.page.size;
+                p.lens[r] = w <= o ? w : int(room < w ? room : w);
+            }
         }
-        p.slots[i] = slot;
-        p.positions[i] = pos;
-    }
-    for (int k = gid; k < taken; k += stride) {
-        const int r = last_at_or_below(s_need, p.N, k);
-        const int held = pages_of(clamped(p.old_lens[r]), p.P);
-        p.table[int64_t(r) * p.M + held + (k - s_need[r])] = popped(k);
-    }
-    // returned pages that this call does not pop again
-    for (int i = gid; i < back && count + i < left; i += stride) p.free_pages[count + i] = returned(i);
-    for (int r = gid; r <= p.N; r += stride) {
-        p.query_start[r] = s_tok[r];
-        if (r == p.N) break;
-        const int o = clamped(p.old_lens[r]), w = clamped(p.new_lens[r]);
-        const int64_t given = min(max(taken - s_need[r], 0), s_need[r + 1] - s_need[r]);
-        const int64_t room = (pages_of(o, p.P) + given) * p.P;
-        p.lens[r] = w <= o ? w : int(room < w ? room : w);
-    }
-    if (gid == 0) {
-        p.info[0] = left;
-        p.info[1] = all.x;
-        p.info[2] = all.y - taken;
-        p.info[3] = taken;
     }
 }
 
@@ -205,7 +204,7 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 // --------------------------------------------------------------------------
 struct AppendParams {
     unsigned rows;  // T * Hkv
-    unsigned Hkv, P;
+    PageDivisor heads, page;
     int64_t num_slots, page_stride, token_stride, head_stride, k_row, v_row;
     float thr;
     const uint16_t* k;
@@ -240,14 +239,31 @@ __device__ __forceinline__ uint4 pack8_bf16(const float (&x)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// x / scale, saturated and rounded to nearest even. A true division, so that the codes
-// are those of the formula at every tie.
+// x / scale, saturated and rounded to nearest even. The quotient is the correctly rounded
+// one, so that the codes are those of the formula at every tie: with y the reciprocal of the
+// scale rounded to nearest, q = x y is corrected once by its remainder (Markstein's division:
+// both steps are fused multiply-adds; this order of the signs keeps that of a zero).
+// Infinities have no remainder, and with a scale below 2^-60 or above 2^60 it could leave the
+// normal numbers: those eight values divide.
 __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float scale) {
+    const float y = __frcp_rn(scale);
+    float q[8], top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        q[i] = x[i] * y;
+        top = fmaxf(top, fabsf(q[i]));
+    }
+    if (top < INFINITY && scale > 0x1p-60f && scale < 0x1p60f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = fmaf(-fmaf(q[i], scale, -x[i]), y, q[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], scale);
+    }
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale)),
-                                        __NV_SATFINITE, __NV_E4M3);
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * i], q[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
@@ -261,44 +277,51 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
     constexpr int LPR = D / 8;
     const unsigned row = blockIdx.x * (kAppendThreads / LPR) + threadIdx.x / LPR;
     const int part = threadIdx.x % LPR;
-    const unsigned t = row / p.Hkv, g = row - t * p.Hkv;
-    const int64_t slot = row < p.rows ? p.slots[t] : -1;
-    const bool live = slot >= 0 && slot < p.num_slots;
-    uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
-    if (live) {
-        ku = __ldcs(reinterpret_cast<const uint4*>(p.k + t * p.k_row + g * D + part * 8));
-        vu = __ldcs(reinterpret_cast<const uint4*>(p.v + t * p.v_row + g * D + part * 8));
+    const unsigned t = p.heads.index(row), g = row - t * p.heads.size;
+    const uint32_t peers = __ballot_sync(0xffffffffu, row < p.rows);
+    if (row >= p.rows) return;  // whole groups leave together
+    // every load at once: a row that is skipped in the end is read too
+    const int64_t slot = p.slots[t];
+    uint4 ku = __ldcs(reinterpret_cast<const uint4*>(p.k + t * p.k_row + g * D + part * 8));
+    const uint4 vu = __ldcs(reinterpret_cast<const uint4*>(p.v + t * p.v_row + g * D + part * 8));
+    float ks = 1.f, vs = 1.f;
+    if constexpr (E4M3) {
+        ks = p.k_scale[g];
+        vs = p.v_scale[g];
     }
     float kx[8];
     if constexpr (CLIP) {
-        unpack8(ku, kx);
-        if (p.clip_scale && live) {
+        float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = a;
+        if (p.clip_scale) {
             const float4* s = reinterpret_cast<const float4*>(p.clip_scale + g * D + part * 8);
-            const float4 a = s[0], b = s[1];
-            kx[0] *= a.x; kx[1] *= a.y; kx[2] *= a.z; kx[3] *= a.w;
-            kx[4] *= b.x; kx[5] *= b.y; kx[6] *= b.z; kx[7] *= b.w;
+            a = s[0];
+            b = s[1];
         }
+        const float tau = p.tau ? p.tau[t] : 1.f;
+        unpack8(ku, kx);
+        kx[0] *= a.x; kx[1] *= a.y; kx[2] *= a.z; kx[3] *= a.w;
+        kx[4] *= b.x; kx[5] *= b.y; kx[6] *= b.z; kx[7] *= b.w;
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(kx[i], kx[i], ss);
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(peers, ss, o);
         const float n = sqrtf(ss);
-        const float c = (n > p.thr ? p.thr / n : 1.f) * (p.tau && live ? p.tau[t] : 1.f);
+        const float c = (n > p.thr ? p.thr / n : 1.f) * tau;
 #pragma unroll
         for (int i = 0; i < 8; ++i) kx[i] *= c;
         ku = pack8_bf16(kx);  // the clip's result is BF16, as inkling_l2clip_fwd's is
     }
-    if (!live) return;
-    const unsigned page = unsigned(slot) / p.P;  // slots are below 2^32
-    const int64_t at = int64_t(page) * p.page_stride + int64_t(unsigned(slot) - page * p.P) * p.token_stride +
+    if (slot < 0 || slot >= p.num_slots) return;
+    const int page = p.page.index(int(slot));  // slots are below 2^31
+    const int64_t at = int64_t(page) * p.page_stride + int64_t(int(slot) - page * p.page.size) * p.token_stride +
                        int64_t(g) * p.head_stride + part * 8;
     if constexpr (E4M3) {
         float vx[8];
         unpack8(ku, kx);
         unpack8(vu, vx);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.k_cache) + at) = pack8_e4m3(kx, p.k_scale[g]);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v_cache) + at) = pack8_e4m3(vx, p.v_scale[g]);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.k_cache) + at) = pack8_e4m3(kx, ks);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v_cache) + at) = pack8_e4m3(vx, vs);
     } else {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.k_cache) + at) = ku;
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.v_cache) + at) = vu;
@@ -329,7 +352,7 @@ inkling_status check_cache(const inkling_kv_cache_desc* c, CacheLayout* out) {
     if (c->dtype != INKLING_KV_BF16 && c->dtype != INKLING_KV_E4M3) return INKLING_ERR_INVALID_ARG;
     if (c->head_dim != 64 && c->head_dim != 128) return INKLING_ERR_UNSUPPORTED;
     if (c->num_pages > 0x7fffffff || c->page_size >= (int64_t(1) << 30) || c->heads_kv >= 65536 ||
-        c->num_pages * c->page_size > (int64_t(1) << 32))
+        c->num_pages * c->page_size > (int64_t(1) << 31))
         return INKLING_ERR_UNSUPPORTED;
     const int64_t unit = c->dtype == INKLING_KV_BF16 ? 8 : 16;
     const int64_t extent[3] = {c->num_pages, c->page_size, c->heads_kv};
@@ -379,7 +402,7 @@ inkling_status inkling_kv_plan(const inkling_kv_plan_dims* dims, const int32_t* 
     if (overlap(block_table, N * size_t(dims->max_pages) * 4, free_pages, size_t(dims->num_pages) * 4))
         return INKLING_ERR_INVALID_ARG;
 
-    PlanParams p{int(N), int(dims->page_size), int(dims->max_pages), int(dims->num_pages), int(T),
+    PlanParams p{int(N), int(dims->max_pages), int(dims->num_pages), int(T), PageDivisor(dims->page_size),
                  old_lens, new_lens, block_table, free_pages, free_count, lens, query_start, slots, positions, info};
     const size_t smem = (N + 1) * 12;
     if (smem > 48 * 1024) {
@@ -387,10 +410,10 @@ inkling_status inkling_kv_plan(const inkling_kv_plan_dims* dims, const int32_t* 
             cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return status_of(e);
     }
-    // Tokens and table entries are spread over at most one block per SM: more would only
-    // repeat the prefix sums.
-    const size_t items = T > N + 1 ? T : N + 1;
-    const size_t want = (items + kPlanThreads - 1) / kPlanThreads;
+    // At most one block per SM: more would only repeat the prefix sums. The pages taken and
+    // returned are not known here; they are fewer than the tokens and requests, or many
+    // rounds of the loop in any case.
+    const size_t want = (T + 2 * N + 1 + kPlanThreads - 1) / kPlanThreads;
     plan_kernel<<<unsigned(want < 148 ? want : 148), kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
     return status_of(cudaGetLastError());
 }
@@ -418,7 +441,7 @@ inkling_status inkling_kv_append(const inkling_kv_cache_desc* cache, const inkli
         !aligned(clip_scale, 16) || !aligned(slots, 8) || !aligned(tau, 4) || !aligned(k_scale, 4) ||
         !aligned(v_scale, 4))
         return INKLING_ERR_INVALID_ARG;
-    AppendParams p{unsigned(T * H), unsigned(H), unsigned(cache->page_size), cache->num_pages * cache->page_size,
+    AppendParams p{unsigned(T * H), PageDivisor(H), PageDivisor(cache->page_size), cache->num_pages * cache->page_size,
                    lay.page_stride, lay.token_stride, lay.head_stride, T > 1 ? dims->k_row : 0,
                    T > 1 ? dims->v_row : 0, float(dims->threshold), k, v, slots, k_scale, v_scale, clip_scale, tau,
                    k_cache, v_cache};

@@ -31,7 +31,7 @@ def dec(**kw):
 
 BAD_CACHE = [(dict(num_pages=0), 1), (dict(page_size=0), 1), (dict(heads_kv=0), 1), (dict(dtype=2), 1),
              (dict(head_dim=96), 2), (dict(num_pages=1 << 31), 2), (dict(page_size=1 << 30), 2),
-             (dict(num_pages=1 << 20, page_size=1 << 13), 2), (dict(head_stride=64), 1), (dict(token_stride=100), 1),
+             (dict(num_pages=1 << 20, page_size=(1 << 11) + 1), 2), (dict(head_stride=64), 1), (dict(token_stride=100), 1),
              (dict(page_stride=-512), 1), (dict(page_stride=0), 1), (dict(head_stride=132), 1),
              (dict(dtype=1, head_stride=136), 1), (dict(page_stride=1 << 58), 2)]
 

@@ -375,6 +375,25 @@ def test_append_copies_or_rounds_exactly(T, H, D, page, dtype, layout):
         assert np.array_equal(got, want)
 
 
+@pytest.mark.parametrize("scale", [0.0107, 1 / 3, 3.0, 1e-3, 7.7e-20, 5e21, 1.9e-37])
+def test_append_e4m3_quotients_are_correctly_rounded(scale):
+    """Every BF16 value, with scales that are no powers of two: the code is that of x / scale rounded
+    to FP32 and then to e4m3."""
+    from learned_relative_gqa_b200 import binding
+    x = torch.arange(1 << 16, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16).view(-1, 1, 64)
+    T = x.shape[0]
+    kc = torch.zeros(T // 16, 16, 1, 64, dtype=torch.float8_e4m3fn, device="cuda")
+    vc = torch.zeros_like(kc)
+    s = torch.tensor([scale], device="cuda")
+    binding.kv_append(x, x, torch.arange(T, device="cuda"), kc, vc, k_scale=s, v_scale=s)
+    with np.errstate(all="ignore"):
+        q = (x.cpu().float().numpy() / np.float32(scale)).astype(np.float64)
+    want = e4m3_codes(q).reshape(-1)
+    for c in (kc, vc):
+        got = c.view(torch.uint8).cpu().numpy().reshape(-1)
+        assert np.array_equal(np.where(got == 0xff, 0x7f, got), np.where(want == 0xff, 0x7f, want))
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("with_scale,with_tau,thr", [(True, True, 8.0), (False, True, 5.0), (True, False, 1e9),
                                                      (False, False, 0.0)])
