@@ -98,6 +98,49 @@ void check_scales(const inkling_kv_cache_desc& c, at::Device device, const at::T
     check(v, "v_scale", device, at::kFloat, {c.heads_kv});
 }
 
+// The outputs of a call as tensors over one allocation, each at a multiple of 256 bytes: a
+// fraction of the host time of as many allocations.
+class Outputs {
+  public:
+    void add(at::ScalarType type, std::initializer_list<int64_t> sizes) {
+        TORCH_INTERNAL_ASSERT(count_ < kMost && sizes.size() <= 3);
+        Item& it = items_[count_++];
+        it.type = type;
+        it.dims = int(sizes.size());
+        int64_t n = int64_t(c10::elementSize(type));
+        int i = 0;
+        for (int64_t s : sizes) {
+            it.sizes[i++] = s;
+            n *= s;
+        }
+        it.at = bytes_;
+        bytes_ += (n + 255) / 256 * 256;
+    }
+    void allocate(at::Device dev) {
+        whole_ = at::empty({bytes_}, at::TensorOptions().dtype(at::kByte).device(dev));
+    }
+    at::Tensor get(int i) const {
+        const Item& it = items_[i];
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole_.storage()), whole_.key_set(),
+                                                                c10::scalarTypeToTypeMeta(it.type));
+        t.unsafeGetTensorImpl()->set_storage_offset(it.at / int64_t(c10::elementSize(it.type)));
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(c10::IntArrayRef(it.sizes, it.dims));
+        return t;
+    }
+
+  private:
+    static constexpr int kMost = 5;
+    struct Item {
+        at::ScalarType type;
+        int dims;
+        int64_t sizes[3], at;
+    };
+    Item items_[kMost];
+    int count_ = 0;
+    int64_t bytes_ = 0;
+    at::Tensor whole_;
+};
+
 PyObject* status(inkling_status s) { return PyLong_FromLong(s); }
 
 // kv_plan(old_lens, new_lens, block_table, free_pages, free_count, page_size, num_pages, max_tokens, lens, info)
@@ -122,10 +165,15 @@ PyObject* kv_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(lens_out, "lens", dev, at::kInt, {N});
     check(info_out, "info", dev, at::kInt, {4});
     const c10::cuda::CUDAGuard guard(dev);
-    const auto i32 = at::TensorOptions().dtype(at::kInt).device(dev);
-    const at::Tensor lens = lens_out ? *lens_out : at::empty({N}, i32), info = info_out ? *info_out : at::empty({4}, i32);
-    const at::Tensor start = at::empty({N + 1}, i32), positions = at::empty({T}, i32);
-    const at::Tensor slots = at::empty({T}, i32.dtype(at::kLong));
+    Outputs outs;
+    outs.add(at::kLong, {T});
+    outs.add(at::kInt, {T});
+    outs.add(at::kInt, {N + 1});
+    if (!lens_out) outs.add(at::kInt, {N});
+    if (!info_out) outs.add(at::kInt, {4});
+    outs.allocate(dev);
+    const at::Tensor slots = outs.get(0), positions = outs.get(1), start = outs.get(2);
+    const at::Tensor lens = lens_out ? *lens_out : outs.get(3), info = info_out ? *info_out : outs.get(lens_out ? 3 : 4);
     const inkling_kv_plan_dims dims{N, page_size, M, num_pages, T};
     const inkling_status s =
         g_plan(&dims, data<int32_t>(&old_lens), data<int32_t>(&new_lens), data<int32_t>(&table), data<int32_t>(&pages),
@@ -200,14 +248,17 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (ws) check(ws, "workspace", dev, at::kByte, {ws->numel()});
     const inkling_rel_attn_decode_dims dims{N, Hq, R, integer(a[7]), M, a[8] == Py_None ? 0.0 : real(a[8])};
     const c10::cuda::CUDAGuard guard(dev);
-    const auto f32 = at::TensorOptions().dtype(at::kFloat).device(dev);
     at::Tensor own;
     if (!ws) {
         const size_t size = g_decode_size(&cache, &dims);
-        if (size != 0) own = at::empty({int64_t(size)}, f32.dtype(at::kByte));
+        if (size != 0) own = at::empty({int64_t(size)}, at::TensorOptions().dtype(at::kByte).device(dev));
         ws = &own;
     }
-    const at::Tensor out = at::empty({N, Hq, D}, f32), lse = at::empty({N, Hq}, f32);
+    Outputs outs;
+    outs.add(at::kFloat, {N, Hq, D});
+    outs.add(at::kFloat, {N, Hq});
+    outs.allocate(dev);
+    const at::Tensor out = outs.get(0), lse = outs.get(1);
     const inkling_status s = g_decode(
         &cache, &dims, data<uint16_t>(&q), kc.data_ptr(), vc.data_ptr(), data<float>(ks), data<float>(vs),
         R ? data<uint16_t>(prof) : nullptr, data<float>(sink), data<int32_t>(&table), data<int32_t>(&lens),
