@@ -193,11 +193,11 @@ __device__ __forceinline__ float weight(float x, float top) { return x == top ? 
 
 enum : int { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8 };  // of a run of tiles of one unit
 
-// Position in the numbered tiles: request, unit of it, tile of that; `at` counts tiles and
-// unit starts from the worker's first one.
+// Position in the numbered tiles: request, unit of it (KV head and block of query heads),
+// tile of that; `at` counts tiles and unit starts from the worker's first one.
 struct Cursor {
     Span s;
-    int n, u, t, next_len, at;
+    int n, kvh, hb, t, next_len, at;
 };
 
 // WHOLE: a CTA for each unit and no split. Its warps take the unit's tiles in turn and join
@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     constexpr int NS = KT / 8;  // S accumulator tiles of 8 keys
     constexpr int STEP = WHOLE ? kWarps : 1;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int4 s_tile[kWarps][ST];    // request, unit, first key, length
-    __shared__ int4 s_flags[kWarps][ST];   // allowed keys of the tile, kFirst .., Cursor::at
+    __shared__ int4 s_tile[kWarps][ST];    // request, KV head, first key, length
+    __shared__ int4 s_flags[kWarps][ST];   // allowed keys of the tile, kFirst .., Cursor::at, first query head
     __shared__ long long s_sum[kWarps];
     __shared__ long long s_base[kWarps];
     __shared__ int s_n[kWarps], s_len[kWarps];
@@ -225,11 +225,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     const uint32_t ring = smem_u32(smem) + warp * S::RING;
 
     Cursor cur{};
-    long long all = 0, first = 0;
-    int limit = 0, worker = 0, workers = 0;
+    // worker w has share tiles (and unit starts), the first `longer` workers one more
+    long long all = 0, first = 0, share = 0;
+    int limit = 0, worker = 0, workers = 0, longer = 0;
+    auto begin_of = [&](int w) { return w * share + min(w, longer); };
     if constexpr (WHOLE) {
         cur.n = blockIdx.x / units;
-        cur.u = blockIdx.x - cur.n * units;
+        cur.kvh = (blockIdx.x - cur.n * units) / p.hblocks;
+        cur.hb = blockIdx.x - cur.n * units - cur.kvh * p.hblocks;
         cur.t = warp;
         cur.s = span_of<KT>(p, p.lens[cur.n]);
     } else {
@@ -257,10 +260,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
         before *= units;
         const long long enough = max(all / S::MIN_TILES, 1ll);
         workers = int(enough < (long long)gridDim.x * kWarps ? enough : (long long)gridDim.x * kWarps);
+        share = all <= 0x7fffffff ? uint32_t(all) / uint32_t(workers) : all / workers;
+        longer = int(all - share * workers);
         // neighbours in the order of the tiles are on different SMs
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const long long from = (long long)(w * gridDim.x + blockIdx.x) * all / workers;
+            const long long from = begin_of(w * gridDim.x + blockIdx.x);
             if (before <= from && from < before + own * units) {
                 long long at = before;
                 int n = n0, len;
@@ -281,14 +286,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
             if (lane == 0) p.rec[worker] = Rec{0, 0, 0};
             return;
         }
-        first = worker * all / workers;
-        limit = int((worker + 1) * all / workers - first);
+        first = begin_of(worker);
+        limit = int(share) + (worker < longer ? 1 : 0);
         cur.n = s_n[warp];
         cur.next_len = cur.n + 1 < p.N ? p.lens[cur.n + 1] : 0;
         cur.s = span_of<KT>(p, s_len[warp]);
         const long long local = first - s_base[warp];
-        cur.u = int(local / (cur.s.tiles + 1));
-        cur.t = int(local - (long long)cur.u * (cur.s.tiles + 1)) - 1;
+        const int u = all <= 0x7fffffff ? int(uint32_t(local) / uint32_t(cur.s.tiles + 1)) : int(local / (cur.s.tiles + 1));
+        cur.kvh = u / p.hblocks;
+        cur.hb = u - cur.kvh * p.hblocks;
+        cur.t = int(local - (long long)u * (cur.s.tiles + 1)) - 1;
         if (cur.t < 0) cur.t = 0, cur.at = 1;  // the range begins with the unit's start
     }
 
@@ -303,8 +310,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
             if (c.t < c.s.tiles) return;
             c.t = 0;
             ++c.at;
-            if (++c.u < units) return;
-            c.u = 0;
+            if (++c.hb < p.hblocks) return;
+            c.hb = 0;
+            if (++c.kvh < p.Hkv) return;
+            c.kvh = 0;
             ++c.n;
             c.s = span_of<KT>(p, c.next_len);
             c.next_len = c.n + 1 < p.N ? p.lens[c.n + 1] : 0;
@@ -314,60 +323,82 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
         const int j = c.s.lo + c.t * KT + my_key;
         return j < c.s.len ? p.table[int64_t(c.n) * p.M + p.page.index(j)] : -1;
     };
+    // Issues a tile's copies. It stands between the products of every tile, so it is kept to few
+    // instructions: no division, and one or two page bases where a tile meets no third page.
     auto issue = [&](const Cursor& c, int i, int stage, int page) {
-        const int j0 = c.s.lo + c.t * KT, j = j0 + my_key;
-        const int kvh = c.u / p.hblocks, hb = c.u - kvh * p.hblocks;
-        const int head0 = kvh * p.group + hb * 8 * NT;
+        const int j0 = c.s.lo + c.t * KT;
+        const int head0 = c.kvh * p.group + c.hb * 8 * NT;
         const bool ok = page >= 0 && page < p.num_pages;
         const uint32_t mask = __ballot_sync(0xffffffffu, ok) & kAll;
         const bool run = i == 0 || (!WHOLE && c.t == 0), ends = c.t == c.s.tiles - 1;
         if (lane == 0) {
-            s_tile[warp][stage] = make_int4(c.n, c.u, j0, c.s.len);
+            s_tile[warp][stage] = make_int4(c.n, c.kvh, j0, c.s.len);
             s_flags[warp][stage] = make_int4(int(mask),
                                              (run ? kFirst : 0) | (ends || c.at + 1 >= limit ? kLast : 0) |
                                                  (c.t == 0 ? kBegins : 0) | (ends ? kEnds : 0),
-                                             c.at, 0);
+                                             c.at, head0);
         }
         const uint32_t dst = ring + stage * S::STAGE;
-        const int offset = j - p.page.index(j) * p.page.size;  // in its page
-        int64_t at = ok ? int64_t(page) * p.page_stride + int64_t(offset) * p.token_stride + kvh * p.head_stride : 0;
         constexpr int ROWS = 32 / S::CPR;  // of a copy of 16 bytes per lane
         const int r0 = lane / S::CPR, ch = lane % S::CPR;
-        if (mask == kAll && __shfl_sync(0xffffffffu, offset, 0) + KT <= p.page.size) {
-            // the usual tile: every key allowed, all in one page, so rows follow each other
-            at = __shfl_sync(0xffffffffu, at, 0) + r0 * p.token_stride + ch * 16;
-            const uint8_t *k = p.k_cache + at, *v = p.v_cache + at;
+        const int64_t head = c.kvh * p.head_stride + ch * 16;
+        const int offset = j0 - p.page.index(j0) * p.page.size;  // of the first key in its page
+        const int split = p.page.size - offset;                  // keys up to that page's end
+        if (p.page.size >= KT) {
+            const int pa = __shfl_sync(0xffffffffu, page, 0), pb = __shfl_sync(0xffffffffu, page, min(split, KT - 1));
+            int64_t a = pa * p.page_stride + (offset + r0) * p.token_stride + head;
+            if (mask == kAll && split >= KT) {  // the usual tile: every key allowed, all in one page
+                const uint8_t *k = p.k_cache + a, *v = p.v_cache + a;
 #pragma unroll
-            for (int x = 0; x < KT / ROWS; ++x) {
-                const int r = x * ROWS + r0;
-                const uint32_t to = dst + r * S::RB + ((ch ^ S::swz(r)) << 4);
-                cp_async_16(to, k, 16u);
-                cp_async_16(to + S::SIDE, v, 16u);
-                k += ROWS * p.token_stride;
-                v += ROWS * p.token_stride;
+                for (int x = 0; x < KT / ROWS; ++x) {
+                    const int r = x * ROWS + r0;
+                    const uint32_t to = dst + r * S::RB + ((ch ^ S::swz(r)) << 4);
+                    cp_async_16(to, k, 16u);
+                    cp_async_16(to + S::SIDE, v, 16u);
+                    k += ROWS * p.token_stride;
+                    v += ROWS * p.token_stride;
+                }
+            } else {
+                int64_t b = pb * p.page_stride + (r0 - split) * p.token_stride + head;
+#pragma unroll
+                for (int x = 0; x < KT / ROWS; ++x) {
+                    const int r = x * ROWS + r0;
+                    const bool in = (mask >> r) & 1u;
+                    const int64_t off = in ? (r < split ? a : b) : 0;
+                    const uint32_t to = dst + r * S::RB + ((ch ^ S::swz(r)) << 4);
+                    cp_async_16(to, p.k_cache + off, in ? 16u : 0u);
+                    cp_async_16(to + S::SIDE, p.v_cache + off, in ? 16u : 0u);
+                    a += ROWS * p.token_stride;
+                    b += ROWS * p.token_stride;
+                }
             }
-        } else {
+        } else {  // pages shorter than a tile: each key's row by itself
+            const int j = j0 + my_key;
+            const int64_t at =
+                ok ? page * p.page_stride + (j - p.page.index(j) * p.page.size) * p.token_stride : 0;
 #pragma unroll
             for (int x = 0; x < KT / ROWS; ++x) {
                 const int r = x * ROWS + r0;
-                const int64_t off = __shfl_sync(0xffffffffu, at, r) + ch * 16;
-                const uint32_t bytes = (mask >> r) & 1u ? 16u : 0u;
+                const bool in = (mask >> r) & 1u;
+                const int64_t row = __shfl_sync(0xffffffffu, at, r);
+                const int64_t off = in ? row + head : 0;
                 const uint32_t to = dst + r * S::RB + ((ch ^ S::swz(r)) << 4);
-                cp_async_16(to, p.k_cache + off, bytes);
-                cp_async_16(to + S::SIDE, p.v_cache + off, bytes);
+                cp_async_16(to, p.k_cache + off, in ? 16u : 0u);
+                cp_async_16(to + S::SIDE, p.v_cache + off, in ? 16u : 0u);
             }
         }
         // profile entries of the distances [dlo, dlo + KT), in whole chunks of 8
         const int dlo = c.s.len - KT - j0;
-        const int heads = min(8 * NT, p.group - hb * 8 * NT);
+        const int heads = min(8 * NT, p.group - c.hb * 8 * NT);
         if (p.R > 0 && dlo < p.R) {
             const int c0 = dlo >> 3;
+            const uint16_t* const first_row = p.profiles + (int64_t(c.n) * p.Hq + head0) * p.R;
 #pragma unroll
             for (int x = lane; x < 8 * NT * S::BCH; x += 32) {
                 const int h = x / S::BCH, ch = c0 + x - h * S::BCH;
                 const bool in = h < heads && ch >= 0 && ch < (p.R >> 3);
-                const int64_t off = in ? (int64_t(c.n) * p.Hq + head0 + h) * p.R + ch * 8 : 0;
-                cp_async_16(dst + 2 * S::SIDE + x * 16, p.profiles + off, in ? 16u : 0u);
+                const int64_t off = in ? int64_t(h) * p.R + ch * 8 : 0;
+                cp_async_16(dst + 2 * S::SIDE + x * 16, first_row + off, in ? 16u : 0u);
             }
         }
         if (!WHOLE && run) {  // q and the sink are loaded when the tile's turn comes: warm L2 for that
@@ -382,11 +413,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
         float sink[NT];
     };
     int head0 = 0, heads = 0;
-    auto place = [&](int u) {
-        const int kvh = u / p.hblocks, hb = u - kvh * p.hblocks;
-        head0 = kvh * p.group + hb * 8 * NT;
-        heads = min(8 * NT, p.group - hb * 8 * NT);
-    };
+    auto heads_from = [&](int kvh, int from) { return min(8 * NT, (kvh + 1) * p.group - from); };
     auto load_query = [&](Query& q, int n, int from, int count) {
 #pragma unroll
         for (int r = 0; r < NT; ++r) {
@@ -409,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     float zscale[NT];
     float o[D / 16][NT][4];
     float mx[NT], sum[NT];
-    auto start = [&](int u) {  // of a unit, its query in qa
+    auto start = [&](int kvh) {  // of a unit, its query in qa
 #pragma unroll
         for (int r = 0; r < NT; ++r) {
             zscale[r] = p.scale_log2;
@@ -437,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
                         const float2 x = unpack2<false>(qa.a[ks][2 * r + y]);
                         qa.a[ks][2 * r + y] = pack2<true>(x.x * down, x.y * down);
                     }
-                zscale[r] *= __uint_as_float(uint32_t(127 + e) << 23) * p.k_scale[u / p.hblocks];
+                zscale[r] *= __uint_as_float(uint32_t(127 + e) << 23) * p.k_scale[kvh];
             }
 #pragma unroll
             for (int m = 0; m < D / 16; ++m)
@@ -447,7 +474,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     };
 
     if constexpr (WHOLE) {
-        place(cur.u);
+        head0 = cur.kvh * p.group + cur.hb * 8 * NT;
+        heads = heads_from(cur.kvh, head0);
         load_query(qa, cur.n, head0, heads);
     }
     int page = -1, made = 0;
@@ -472,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
         cur = at[ST - 1];
         page = pages[ST - 1];
     }
-    if constexpr (WHOLE) start(cur.u);
+    if constexpr (WHOLE) start(cur.kvh);
 
     [[maybe_unused]] Query qn;  // the next unit's query, where registers allow
     [[maybe_unused]] bool begins = false;
@@ -493,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
         if constexpr (!WHOLE) {
             if (flags & kFirst) {
                 begins = flags & kBegins;
-                place(tile.y);
+                head0 = info.w;
+                heads = heads_from(tile.y, head0);
                 if (NT == 1 && i > 0) qa = qn;
                 else load_query(qa, tile.x, head0, heads);
                 start(tile.y);
@@ -501,8 +530,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
             // one group of heads leaves the registers to have the next unit's query on its way
             if (NT == 1 && had_next && (s_flags[warp][ahead].y & kFirst)) {
                 const int4 next = s_tile[warp][ahead];
-                const int kvh = next.y / p.hblocks, hb = next.y - kvh * p.hblocks;
-                load_query(qn, next.x, kvh * p.group + hb * 8 * NT, min(8 * NT, p.group - hb * 8 * NT));
+                const int from = s_flags[warp][ahead].w;
+                load_query(qn, next.x, from, heads_from(next.y, from));
             }
         }
         stage = ahead;
@@ -676,9 +705,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
 
         if constexpr (!WHOLE) {
             if (flags & kLast) {
-                const int n = tile.x, u = tile.y;
+                const int n = tile.x;
                 const bool ends = flags & kEnds, whole = begins && ends;
-                const float vs = F8 ? p.v_scale[u / p.hblocks] : 1.f;
+                const float vs = F8 ? p.v_scale[tile.y] : 1.f;
                 const int slot = 2 * worker + (begins ? 1 : 0);
 #pragma unroll
                 for (int r = 0; r < NT; ++r) {
@@ -722,8 +751,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
                     // the worker of the unit's last tile, which is tiles - 1 - t behind this one
                     const Span sp = span_of<KT>(p, tile.w);
                     const long long rest = sp.tiles - 1 - (tile.z - sp.lo) / KT;
-                    rec = Rec{int64_t(n) * p.Hq + head0, heads,
-                              int(((first + info.z + rest + 1) * workers - 1) / all) - worker};
+                    const long long at = first + info.z + rest, split = longer * (share + 1);
+                    const int owner = int(at < split ? at / (share + 1) : longer + (at - split) / share);
+                    rec = Rec{int64_t(n) * p.Hq + head0, heads, owner - worker};
                 }
             }
         }
@@ -734,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     } else {
         // ---- join the four warps through their rings, which are free now
         cp_async_wait_group<0>();
-        const int n = blockIdx.x / units, u = blockIdx.x - n * units;
+        const int n = cur.n;
 #pragma unroll
         for (int r = 0; r < NT; ++r) {
             sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
@@ -754,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
                     mine[h * S::OROW + d] = o[m][r][e];
                 }
         __syncthreads();
-        const float vs = F8 ? p.v_scale[u / p.hblocks] : 1.f;
+        const float vs = F8 ? p.v_scale[cur.kvh] : 1.f;
         for (int it = tid; it < heads * (D / 4); it += kThreads) {
             const int h = it / (D / 4), d = (it - h * (D / 4)) * 4;
             const int64_t at = int64_t(n) * p.Hq + head0 + h;
