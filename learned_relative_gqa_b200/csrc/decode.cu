@@ -54,13 +54,13 @@ namespace {
 using namespace ira;
 
 constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 320;
 constexpr int kMaxWorkers = kMaxCtas * kWarps;  // workspace slots: two per worker
-// One CTA per unit, with no split, up to these sizes: tiles of a unit and units of the call.
-constexpr int kWholeTiles = 32;
-constexpr int kWholeUnits = 1024;
+// One CTA per unit, with no split, up to these sizes: tiles of each of its warps, and units
+// of the call.
+constexpr int kWholeTiles = 8;
+constexpr int kWholeUnits = 512;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinBatch = 6;                   // parts that a lane of it loads at once
 
@@ -162,7 +162,6 @@ struct Shape {
     // 13.1 us with 4; 32768 tokens, 1 x 16 heads 22.1 us with 2 and 18.5 us with 4.
     static constexpr int MIN_TILES = 2 * NT;
     static constexpr int RING = STAGES * STAGE;
-    static constexpr int SMEM = kWarps * RING;
     static constexpr int OROW = D + 4;                      // floats of a head's row when warps join (no bank conflicts)
     static_assert(8 * NT * OROW * 4 <= RING, "the rings hold the warps' results when they join");
     // chunk c of row r stands at chunk c ^ swz(r): ldmatrix's eight rows use all banks
@@ -200,24 +199,26 @@ struct Cursor {
     int n, kvh, hb, t, next_len, at;
 };
 
-// WHOLE: a CTA for each unit and no split. Its warps take the unit's tiles in turn and join
-// through shared memory: no prefix sums at the start, no second kernel at the end.
-// Otherwise the grid's warps are workers with an even share each of all tiles. A unit counts
+// WHOLE (4 or 8 warps): a CTA for each unit and no split. Its warps take the unit's tiles in
+// turn and join through shared memory: no prefix sums at the start, no second kernel at the
+// end. WHOLE == 0: the grid's warps are workers with an even share each of all tiles. A unit counts
 // one more than its tiles there, which is about what loading its query and writing its
 // result take, so that runs of short requests are not the last to finish.
-template <class S, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __grid_constant__ DecodeParams p) {
+template <class S, int WHOLE>
+__global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 : kCtasPerSm)
+    decode_kernel(const __grid_constant__ DecodeParams p) {
+    constexpr int WARPS = WHOLE ? WHOLE : kWarps, THREADS = 32 * WARPS;
     constexpr int D = S::D, NT = S::NT, KT = S::KT, ST = S::STAGES;
     constexpr bool F8 = S::F8;
     constexpr int NS = KT / 8;  // S accumulator tiles of 8 keys
-    constexpr int STEP = WHOLE ? kWarps : 1;
+    constexpr int STEP = WHOLE ? WARPS : 1;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int4 s_tile[kWarps][ST];    // request, KV head, first key, length
-    __shared__ int4 s_flags[kWarps][ST];   // allowed keys of the tile, kFirst .., Cursor::at, first query head
-    __shared__ long long s_sum[kWarps];
-    __shared__ long long s_base[kWarps];
-    __shared__ int s_n[kWarps], s_len[kWarps];
-    __shared__ float2 s_ml[kWarps][8 * NT];
+    __shared__ int4 s_tile[WARPS][ST];    // request, KV head, first key, length
+    __shared__ int4 s_flags[WARPS][ST];   // allowed keys of the tile, kFirst .., Cursor::at, first query head
+    __shared__ long long s_sum[WARPS];
+    __shared__ long long s_base[WARPS];
+    __shared__ int s_n[WARPS], s_len[WARPS];
+    __shared__ float2 s_ml[WARPS][8 * NT];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     } else {
         // the joining kernel may be set up now; it waits for this one's results itself
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        const int chunk = (p.N + kThreads - 1) / kThreads;
+        const int chunk = (p.N + THREADS - 1) / THREADS;
         const int n0 = min(tid * chunk, p.N), n1 = min(n0 + chunk, p.N);
         long long own = 0;
         for (int n = n0; n < n1; ++n) own += span_of<KT>(p, p.lens[n]).tiles + 1;
@@ -252,19 +253,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
         __syncthreads();
         long long before = inc - own;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             if (w < warp) before += s_sum[w];
             all += s_sum[w];
         }
         all *= units;
         before *= units;
         const long long enough = max(all / S::MIN_TILES, 1ll);
-        workers = int(enough < (long long)gridDim.x * kWarps ? enough : (long long)gridDim.x * kWarps);
+        workers = int(enough < (long long)gridDim.x * WARPS ? enough : (long long)gridDim.x * WARPS);
         share = all <= 0x7fffffff ? uint32_t(all) / uint32_t(workers) : all / workers;
         longer = int(all - share * workers);
         // neighbours in the order of the tiles are on different SMs
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             const long long from = begin_of(w * gridDim.x + blockIdx.x);
             if (before <= from && from < before + own * units) {
                 long long at = before;
@@ -762,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     if constexpr (!WHOLE) {
         if (lane == 0) p.rec[worker] = rec;
     } else {
-        // ---- join the four warps through their rings, which are free now
+        // ---- join the warps through their rings, which are free now
         cp_async_wait_group<0>();
         const int n = cur.n;
 #pragma unroll
@@ -785,14 +786,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
                 }
         __syncthreads();
         const float vs = F8 ? p.v_scale[cur.kvh] : 1.f;
-        for (int it = tid; it < heads * (D / 4); it += kThreads) {
+        for (int it = tid; it < heads * (D / 4); it += THREADS) {
             const int h = it / (D / 4), d = (it - h * (D / 4)) * 4;
             const int64_t at = int64_t(n) * p.Hq + head0 + h;
             const float sk = p.sink ? p.sink[at] * kLog2e : -INFINITY;
-            float2 ml[kWarps];
+            float2 ml[WARPS];
             float m = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < WARPS; ++w) {
                 ml[w] = s_ml[w][h];
                 m = fmaxf(m, ml[w].x);
             }
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
             float l = top == -INFINITY ? 0.f : weight(sk, top);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < WARPS; ++w) {
                 const float f = weight(ml[w].x, top);
                 const float4 x = *reinterpret_cast<const float4*>(smem + w * S::RING + (h * S::OROW + d) * 4);
                 l = fmaf(ml[w].y, f, l);
@@ -819,31 +820,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
 
 // Joins the parts of each unit that the even split of the tiles cut. Its parts are the
 // second slot of the worker that began it and the first slots of the next `more` workers,
-// in the order of the keys; blockIdx.y is the query head of the unit. All latency, of loads
-// and of the code itself, which is never in the caches: so two short kernels.
-// CHAINS == false: a warp for each worker's record takes all parts, 16 bytes to a lane.
-// CHAINS (few units, each with many parts): a block for 32 workers' records and
-// blockIdx.z's 32 columns; the warps' quarters take the parts in turn, whole 128-byte lines
-// each, and join by shuffles and through shared memory.
-template <int D, bool CHAINS>
+// in the order of the keys. Four blocks (blockIdx.z) read the records of 32 workers and take
+// query head blockIdx.y of the units that those began and did not finish. Where these are
+// one or two, so that their chains of parts may be long, each block takes a quarter of the
+// columns and shares the parts out among all its warps and groups of lanes; where they are
+// more, each warp takes a unit. All latency, of loads and of the code itself, which is never
+// in the caches: so one short kernel.
+template <int D>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams p,
                                                                    int workers) {
     constexpr int WARPS = kJoinThreads / 32;
-    constexpr int LANES = CHAINS ? 8 : D / 4;      // that hold a part's columns
-    constexpr int GROUPS = CHAINS ? 4 * WARPS : 32 / LANES;  // parts at a time
-    __shared__ float4 s_acc[WARPS][8];
+    static_assert(WARPS * 4 == 32, "four blocks have a warp for each of 32 workers");
+    __shared__ float4 s_acc[WARPS][D / 16];
     __shared__ float2 s_ml[WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
-    const int w0 = CHAINS ? blockIdx.x * 32 : blockIdx.x * WARPS + warp;
-    const int group = (CHAINS ? warp * 4 : 0) + lane / LANES;
-    const int d = (CHAINS ? blockIdx.z * 32 : 0) + lane % LANES * 4;
+    const int w0 = blockIdx.x * 32;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     int4 rec = make_int4(0, 0, 0, 0);
-    if (w0 + (CHAINS ? lane : 0) < workers)
-        rec = *reinterpret_cast<const int4*>(p.rec + w0 + (CHAINS ? lane : 0));
-    uint32_t owners = __ballot_sync(0xffffffffu, rec.w > 0 && h < rec.z) & (CHAINS ? 0xffffffffu : 1u);
-    for (; owners != 0; owners &= owners - 1) {
+    if (w0 + lane < workers) rec = *reinterpret_cast<const int4*>(p.rec + w0 + lane);
+    uint32_t owners = __ballot_sync(0xffffffffu, rec.w > 0 && h < rec.z);
+    const bool together = __popc(owners) <= 2;
+    if (!together)
+        for (int x = blockIdx.z * WARPS + warp; x > 0; --x) owners &= owners - 1;
+    const int lanes = together ? D / 16 : D / 4;  // that hold a part's columns
+    const int groups = 32 / lanes * (together ? WARPS : 1), group = lane / lanes + (together ? warp * (32 / lanes) : 0);
+    const int column = lane & (lanes - 1), d = (together ? blockIdx.z * (D / 4) : 0) + column * 4;
+    for (; owners != 0; owners = together ? owners & (owners - 1) : 0u) {
         const int src = __ffs(owners) - 1;
         const int64_t row = (int64_t(__shfl_sync(0xffffffffu, rec.y, src)) << 32) +
                             uint32_t(__shfl_sync(0xffffffffu, rec.x, src)) + h;
@@ -851,12 +854,12 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
         const float sk = p.sink ? p.sink[row] * kLog2e : -INFINITY;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float m = -INFINITY, l = 0.f;
-        for (int x0 = group; x0 < parts; x0 += kJoinBatch * GROUPS) {
+        for (int x0 = group; x0 < parts; x0 += kJoinBatch * groups) {
             float2 ml[kJoinBatch];
             float4 y[kJoinBatch];
 #pragma unroll
             for (int k = 0; k < kJoinBatch; ++k) {
-                const int x = x0 + k * GROUPS;
+                const int x = x0 + k * groups;
                 ml[k] = make_float2(-INFINITY, 0.f);
                 y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (x < parts) {
@@ -886,21 +889,20 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
             l = l * f + ml.y * w;
             acc = make_float4(acc.x * f + y.x * w, acc.y * f + y.y * w, acc.z * f + y.z * w, acc.w * f + y.w * w);
         };
-#pragma unroll
-        for (int o = LANES; o < 32; o <<= 1)
+        for (int o = lanes; o < 32; o <<= 1)
             take(make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o)),
                  make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
                              __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o)));
-        if constexpr (CHAINS) {
+        if (together) {
             __syncthreads();
-            if (lane < LANES) s_acc[warp][lane] = acc;
+            if (lane < lanes) s_acc[warp][lane] = acc;
             if (lane == 0) s_ml[warp] = make_float2(m, l);
             __syncthreads();
             if (warp != 0) continue;
 #pragma unroll 1
-            for (int x = 1; x < WARPS; ++x) take(s_ml[x], s_acc[x][lane % LANES]);
+            for (int x = 1; x < WARPS; ++x) take(s_ml[x], s_acc[x][column]);
         }
-        if (lane >= LANES) continue;
+        if (lane >= lanes) continue;
         const float top = fmaxf(m, sk);
         const float f = weight(m, top);
         const float tot = top == -INFINITY ? 0.f : l * f + weight(sk, top);
@@ -959,27 +961,23 @@ cudaError_t launch_decode(DecodeParams& p, cudaStream_t st) {
     const int span = p.W > 0 && p.W < p.cap ? p.W : p.cap;
     const int64_t unit_tiles = (span + S::KT - 1) / S::KT;
     const int64_t units = int64_t(p.N) * p.Hkv * p.hblocks;
-    if (unit_tiles <= kWholeTiles && units <= kWholeUnits) {
-        e = cudaFuncSetAttribute(decode_kernel<S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-        if (e != cudaSuccess) return e;
-        decode_kernel<S, true><<<unsigned(units), kThreads, S::SMEM, st>>>(p);
+    auto launch = [&](auto kernel, int64_t grid, int warps) {
+        cudaError_t r =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, warps * S::RING);
+        if (r != cudaSuccess) return r;
+        kernel<<<unsigned(grid), 32 * warps, warps * S::RING, st>>>(p);
         return cudaGetLastError();
-    }
-    e = cudaFuncSetAttribute(decode_kernel<S, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-    if (e != cudaSuccess) return e;
+    };
+    if (unit_tiles <= 8 * kWholeTiles && unit_tiles > 4 && units <= sms) return launch(decode_kernel<S, 8>, units, 8);
+    if (unit_tiles <= 4 * kWholeTiles && units <= kWholeUnits) return launch(decode_kernel<S, 4>, units, 4);
     const int64_t workers = std::max<int64_t>(units * (unit_tiles + 1) / S::MIN_TILES, 1);
     int64_t grid = int64_t(sms) * kCtasPerSm;
     if (grid > kMaxCtas) grid = kMaxCtas;
     if (grid > (workers + kWarps - 1) / kWarps) grid = (workers + kWarps - 1) / kWarps;
-    decode_kernel<S, false><<<unsigned(grid), kThreads, S::SMEM, st>>>(p);
-    e = cudaGetLastError();
+    e = launch(decode_kernel<S, 0>, grid, kWarps);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    // few units make long chains of parts (16 and more at least in the mean)
-    const bool chains = units * 16 <= grid * kWarps;
-    const int window = chains ? 32 : kJoinThreads / 32;
-    cfg.gridDim = dim3(unsigned((grid * kWarps + window - 1) / window), unsigned(p.unit_heads),
-                       chains ? S::D / 32 : 1);
+    cfg.gridDim = dim3(unsigned((grid * kWarps + 31) / 32), unsigned(p.unit_heads), 4);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at{};
@@ -987,8 +985,7 @@ cudaError_t launch_decode(DecodeParams& p, cudaStream_t st) {
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, chains ? decode_join_kernel<S::D, true> : decode_join_kernel<S::D, false>,
-                              DecodeParams(p), int(grid) * kWarps);
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel<S::D>, DecodeParams(p), int(grid) * kWarps);
 }
 
 template <int D, bool F8>

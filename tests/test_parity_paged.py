@@ -170,7 +170,7 @@ def test_decode_one_request_over_all_workers(hq, hkv, d, dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_decode_many_units_without_a_split(dtype):
     """A table of few tiles and more units than CTAs on the device: both sides of the limit of the whole form."""
-    for n in (512, 513):
+    for n in (256, 257):
         x, s = problem([(7 * i) % 50 for i in range(n)], 4, 2, 64, 16, 8, dtype, seed=n)
         check(x, s)
 
