@@ -97,7 +97,7 @@ inkling_status inkling_kv_plan(const inkling_kv_plan_dims* dims, const int32_t* 
 /*
  * Appends T rows to the cache: k_cache[slots[t]] = k[t], v_cache[slots[t]] = v[t].
  * Rows whose slot is outside [0, num_pages * page_size) are skipped. Slots that are
- * stored must differ from each other.
+ * stored must differ from each other, and the pools may not overlap.
  *   tokens       T
  *   k_row, v_row elements from one token's [Hkv, D] rows to the next one's, multiples
  *                of 8 and at least Hkv * D (the rows of a fused projection)
@@ -150,7 +150,9 @@ typedef struct {
 } inkling_rel_attn_decode_dims;
 
 /* Bytes of device workspace of inkling_rel_attn_decode; its contents need not be
- * set and mean nothing afterwards. 0 when the sizes are malformed. */
+ * set and mean nothing afterwards. Calls that follow each other may share one (two
+ * captured graphs too, replayed one after the other), calls that can overlap on the
+ * GPU need one each. 0 when the sizes are malformed. */
 size_t inkling_rel_attn_decode_workspace_size(const inkling_kv_cache_desc* cache,
                                               const inkling_rel_attn_decode_dims* dims);
 

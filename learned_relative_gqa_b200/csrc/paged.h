@@ -59,7 +59,9 @@ cudaError_t launch_early(void (*kernel)(A...), dim3 grid, unsigned threads, size
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e != cudaSuccess) (void)cudaGetLastError();  // returned here: leave nothing behind for later checks
+    return e;
 }
 #endif
 

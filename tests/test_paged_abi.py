@@ -98,7 +98,7 @@ def test_append_refusals(lib):
 
     # k, v, slots, k_scale, v_scale, clip_scale, tau, k_cache, v_cache
     def call(change=(), c=None, tokens=5, k_row=512, v_row=512, clip=0, thr=0.0):
-        a = [FAKE, FAKE, FAKE, None, None, None, None, FAKE, FAKE]
+        a = [FAKE, FAKE, FAKE, None, None, None, None, FAKE, ctypes.c_void_p(0x20000)]
         for i, v in dict(change).items():
             a[i] = v
         c = cache() if c is None else c
@@ -110,6 +110,7 @@ def test_append_refusals(lib):
     for i in (0, 1, 7, 8):
         assert call({i: MIS}) == 1, i
     assert call({2: ctypes.c_void_p(0x10004)}) == 1
+    assert call({8: FAKE}) == 1                                          # one pool for both
     assert call(tokens=-1) == 1
     assert call(k_row=511) == 1 and call(v_row=516) == 1 and call(k_row=256) == 1
     assert call({5: FAKE}) == 1 and call({6: FAKE}) == 1                 # clip arguments without the clip

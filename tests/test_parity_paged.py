@@ -321,6 +321,59 @@ def test_decode_captured_and_replayed_with_other_lengths():
             check(x, s, window, got=got)
 
 
+def test_decode_captured_with_forks_and_joins():
+    """Two streams inside one capture, each with two calls, joined before a last one: launches that may
+    overlap their predecessor must still wait for all that the capture orders before them."""
+    from learned_relative_gqa_b200 import binding
+    x, s = problem([900, 30, 0, 411], 8, 2, 64, 16, 32, seed=17)
+    y, t = problem([350, 1200], 4, 1, 128, 32, 0, "e4m3", seed=18)
+    for a, b in ((x, s), (y, t)):
+        binding.paged_decode(**a, **b)
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    got = {}
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        got["a"] = binding.paged_decode(**x, **s)
+        with torch.cuda.stream(side):
+            got["b"] = binding.paged_decode(**y, **t)
+            got["c"] = binding.paged_decode(**y, **t, window=100)
+        got["d"] = binding.paged_decode(**x, **s, window=50)
+        main.wait_stream(side)
+        got["e"] = binding.paged_decode(**x, **s, window=7)
+    for _ in range(3):
+        for pair in got.values():
+            for z in pair:
+                z.fill_(float("nan"))
+        g.replay()
+        check(x, s, got=got["a"])
+        check(y, t, got=got["b"])
+        check(y, t, 100, got=got["c"])
+        check(x, s, 50, got=got["d"])
+        check(x, s, 7, got=got["e"])
+
+
+def test_decode_waits_for_the_kernel_before_it():
+    """Calls back to back with the kernels that write their inputs, and with kernels of other
+    libraries between: each reads what was written last."""
+    from learned_relative_gqa_b200 import binding
+    x, s = problem([1500, 700, 20], 8, 2, 128, 16, 64, seed=19)
+    want = binding.paged_decode(**x, **s)
+    lens, q = x["lens"].clone(), x["q"].clone()
+    wrong = torch.randn_like(x["q"].float()).to(torch.bfloat16)
+    for _ in range(30):
+        x["lens"].fill_(3)
+        x["q"].copy_(wrong)
+        binding.paged_decode(**x, **s)
+        x["lens"].copy_(lens)
+        x["q"].copy_(q)
+        got = binding.paged_decode(**x, **s)
+        again = binding.paged_decode(**x, **s)
+        for a, b in ((got, want), (again, want)):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 # --------------------------------------------------------------------------
 # append
 # --------------------------------------------------------------------------
