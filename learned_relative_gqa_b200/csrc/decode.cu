@@ -220,8 +220,8 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
     constexpr int NS = KT / 8;  // S accumulator tiles of 8 keys
     constexpr int STEP = WHOLE ? WARPS : 1;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int4 s_tile[WARPS][ST];    // request, KV head, first key, length
-    __shared__ int4 s_flags[WARPS][ST];   // allowed keys of the tile, kFirst .., Cursor::at, first query head
+    __shared__ int4 s_tile[WARPS][ST];  // allowed keys, kFirst .., distance of the last key (dlo), Cursor::at
+    __shared__ int4 s_run[WARPS][ST];   // of a run's first tile: request, KV head, first query head, length
     __shared__ long long s_sum[WARPS];
     __shared__ long long s_base[WARPS];
     __shared__ int s_n[WARPS], s_len[WARPS];
@@ -339,12 +339,13 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
         const bool ok = page >= 0 && page < p.num_pages;
         const uint32_t mask = __ballot_sync(0xffffffffu, ok) & kAll;
         const bool run = i == 0 || (!WHOLE && c.t == 0), ends = c.t == c.s.tiles - 1;
+        const int dlo = c.s.len - KT - j0;  // distance of the tile's last key
         if (lane == 0) {
-            s_tile[warp][stage] = make_int4(c.n, c.kvh, j0, c.s.len);
-            s_flags[warp][stage] = make_int4(int(mask),
-                                             (run ? kFirst : 0) | (ends || c.at + 1 >= limit ? kLast : 0) |
-                                                 (c.t == 0 ? kBegins : 0) | (ends ? kEnds : 0),
-                                             c.at, head0);
+            s_tile[warp][stage] = make_int4(int(mask),
+                                            (run ? kFirst : 0) | (ends || c.at + 1 >= limit ? kLast : 0) |
+                                                (c.t == 0 ? kBegins : 0) | (ends ? kEnds : 0),
+                                            dlo, c.at);
+            if (run) s_run[warp][stage] = make_int4(c.n, c.kvh, head0, c.s.len);
         }
         const uint32_t dst = ring + stage * S::STAGE;
         constexpr int ROWS = 32 / S::CPR;  // of a copy of 16 bytes per lane
@@ -408,7 +409,6 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
             }
         }
         // profile entries of the distances [dlo, dlo + KT), in whole chunks of 8
-        const int dlo = c.s.len - KT - j0;
         const int heads = min(8 * NT, p.group - c.hb * 8 * NT);
         if (p.R > 0 && dlo < p.R) {
             const int c0 = dlo >> 3;
@@ -432,7 +432,8 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
         uint32_t a[D / 16][2 * NT];
         float sink[NT];
     };
-    int head0 = 0, heads = 0;
+    int heads = 0;  // query heads of the unit
+    auto first_head = [&](const Cursor& c) { return c.kvh * p.group + c.hb * 8 * NT; };
     auto heads_from = [&](int kvh, int from) { return min(8 * NT, (kvh + 1) * p.group - from); };
     auto load_query = [&](Query& q, int n, int from, int count) {
 #pragma unroll
@@ -485,6 +486,7 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
                         qa.a[ks][2 * r + y] = pack2<true>(x.x * down, x.y * down);
                     }
                 zscale[r] *= __uint_as_float(uint32_t(127 + e) << 23) * p.k_scale[kvh];
+                if (zscale[r] == 0.f) zscale[r] = 0x1p-126f;  // masked entries are -inf times this
             }
 #pragma unroll
             for (int m = 0; m < D / 16; ++m)
@@ -494,9 +496,8 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
     };
 
     if constexpr (WHOLE) {
-        head0 = cur.kvh * p.group + cur.hb * 8 * NT;
-        heads = heads_from(cur.kvh, head0);
-        load_query(qa, cur.n, head0, heads);
+        heads = heads_from(cur.kvh, first_head(cur));
+        load_query(qa, cur.n, first_head(cur), heads);
     }
     int page = -1, made = 0;
     {
@@ -524,6 +525,7 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
 
     [[maybe_unused]] Query qn;  // the next unit's query, where registers allow
     [[maybe_unused]] bool begins = false;
+    [[maybe_unused]] int4 run = make_int4(0, 0, 0, 0);
     Rec rec{0, 0, 0};
 
     int stage = 0;
@@ -533,25 +535,23 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
         const int behind = stage == 0 ? ST - 1 : stage - 1, ahead = stage == ST - 1 ? 0 : stage + 1;
         const bool had_next = i + 1 < made;
         const int4 tile = s_tile[warp][stage];
-        const int4 info = s_flags[warp][stage];
-        const uint32_t mask = uint32_t(info.x);
-        const int flags = info.y;
+        const uint32_t mask = uint32_t(tile.x);
+        const int flags = tile.y, dlo = tile.z;
         const uint32_t kbase = ring + stage * S::STAGE, vbase = kbase + S::SIDE, bbase = vbase + S::SIDE;
 
         if constexpr (!WHOLE) {
             if (flags & kFirst) {
                 begins = flags & kBegins;
-                head0 = info.w;
-                heads = heads_from(tile.y, head0);
+                run = s_run[warp][stage];
+                heads = heads_from(run.y, run.z);
                 if (NT == 1 && i > 0) qa = qn;
-                else load_query(qa, tile.x, head0, heads);
-                start(tile.y);
+                else load_query(qa, run.x, run.z, heads);
+                start(run.y);
             }
             // one group of heads leaves the registers to have the next unit's query on its way
-            if (NT == 1 && had_next && (s_flags[warp][ahead].y & kFirst)) {
-                const int4 next = s_tile[warp][ahead];
-                const int from = s_flags[warp][ahead].w;
-                load_query(qn, next.x, from, heads_from(next.y, from));
+            if (NT == 1 && had_next && (s_tile[warp][ahead].y & kFirst)) {
+                const int4 next = s_run[warp][ahead];
+                load_query(qn, next.x, next.z, heads_from(next.y, next.z));
             }
         }
         stage = ahead;
@@ -572,12 +572,12 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
             const int lrow = (lane & 7) + ((lane >> 4) << 3), lch = (lane >> 3) & 1;
             const int lswz = S::swz(lane & 7);
 
-            // ---- S = Q K^T, in two sums to halve the chain of dependent products
-            float s[NS][4], s2[NS][4];
+            // ---- S = Q K^T
+            float s[NS][4];
 #pragma unroll
             for (int x = 0; x < NS; ++x)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[x][e] = s2[x][e] = 0.f;
+                for (int e = 0; e < 4; ++e) s[x][e] = 0.f;
 #pragma unroll
             for (int c = 0; c < S::CPR / 2; ++c) {  // pairs of 16-byte chunks
 #pragma unroll
@@ -586,34 +586,28 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
                     ldmatrix_x4(kbase + (kk * 16 + lrow) * S::RB + (((2 * c + lch) ^ lswz) << 4), f);
                     if constexpr (!F8) {
                         const uint32_t a1 = NT == 2 ? qa.a[c][2 * (NT - 1)] : 0u, a3 = NT == 2 ? qa.a[c][2 * NT - 1] : 0u;
-                        float(&to)[NS][4] = c % 2 ? s2 : s;
-                        mma16816<false>(to[2 * kk], qa.a[c][0], a1, qa.a[c][1], a3, f[0], f[1]);
-                        mma16816<false>(to[2 * kk + 1], qa.a[c][0], a1, qa.a[c][1], a3, f[2], f[3]);
+                        mma16816<false>(s[2 * kk], qa.a[c][0], a1, qa.a[c][1], a3, f[0], f[1]);
+                        mma16816<false>(s[2 * kk + 1], qa.a[c][0], a1, qa.a[c][1], a3, f[2], f[3]);
                     } else {
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {  // the pair's two chunks: 16 columns each
                             const uint32_t* a = qa.a[2 * c + x];
                             const uint32_t a1 = NT == 2 ? a[2 * (NT - 1)] : 0u, a3 = NT == 2 ? a[2 * NT - 1] : 0u;
-                            float(&to)[NS][4] = x ? s2 : s;
                             uint32_t b0, b1, b2, b3;
                             e4m3x4_to_f16x4(f[x], b0, b1);
                             e4m3x4_to_f16x4(f[x + 2], b2, b3);
-                            mma16816<true>(to[2 * kk], a[0], a1, a[1], a3, b0, b1);
-                            mma16816<true>(to[2 * kk + 1], a[0], a1, a[1], a3, b2, b3);
+                            mma16816<true>(s[2 * kk], a[0], a1, a[1], a3, b0, b1);
+                            mma16816<true>(s[2 * kk + 1], a[0], a1, a[1], a3, b2, b3);
                         }
                     }
                 }
             }
             produce();
 
-            // ---- logits in log2 units, their maximum, the running state
+            // ---- logits in log2 units are s zs; with profile entries they are made here
+            float zs[NT];
 #pragma unroll
-            for (int r = 0; r < NT; ++r)
-#pragma unroll
-                for (int x = 0; x < NS; ++x)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) s[x][2 * r + e] = (s[x][2 * r + e] + s2[x][2 * r + e]) * zscale[r];
-            const int dlo = tile.w - KT - tile.z;
+            for (int r = 0; r < NT; ++r) zs[r] = zscale[r];
             if (p.R > 0 && dlo < p.R) {
 #pragma unroll
                 for (int r = 0; r < NT; ++r) {
@@ -624,7 +618,8 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
                             s[x][2 * r + e] = fmaf(__uint_as_float(lds_u16(at - (8 * x + e) * 2) << 16), kLog2e,
-                                                   s[x][2 * r + e]);
+                                                   s[x][2 * r + e] * zs[r]);
+                    zs[r] = 1.f;
                 }
             }
             if (mask != kAll) {
@@ -636,6 +631,8 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
                         for (int e = 0; e < 2; ++e)
                             if (!((mask >> (8 * x + 2 * t + e)) & 1u)) s[x][2 * r + e] = -INFINITY;
             }
+            // ---- the running maximum moves only when a logit passes it by 2^8, which each lane
+            // sees for its own entries: no exchange in the usual tile
             float top[NT];
             bool grows = false;
 #pragma unroll
@@ -643,13 +640,14 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
                 top[r] = -INFINITY;
 #pragma unroll
                 for (int x = 0; x < NS; ++x) top[r] = fmax3(top[r], s[x][2 * r], s[x][2 * r + 1]);
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+                top[r] *= zs[r];
                 grows |= top[r] > mx[r] + kRescaleThreshold;
             }
             if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
                 for (int r = 0; r < NT; ++r) {
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
                     const float now = fmaxf(mx[r], top[r]);
                     const float f = weight(mx[r], now);
                     mx[r] = now;
@@ -672,7 +670,8 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
                 const float ref = mx[r] == -INFINITY ? 0.f : mx[r];
 #pragma unroll
                 for (int x = 0; x < NS; ++x) {
-                    float p0 = ex2_approx(s[x][2 * r] - ref), p1 = ex2_approx(s[x][2 * r + 1] - ref);
+                    float p0 = ex2_approx(fmaf(s[x][2 * r], zs[r], -ref));
+                    float p1 = ex2_approx(fmaf(s[x][2 * r + 1], zs[r], -ref));
                     sum[r] += p0 + p1;
 #pragma unroll
                     for (int k = 0; k < TERMS; ++k) {
@@ -725,9 +724,9 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
 
         if constexpr (!WHOLE) {
             if (flags & kLast) {
-                const int n = tile.x;
+                const int n = run.x, head0 = run.z;
                 const bool ends = flags & kEnds, whole = begins && ends;
-                const float vs = F8 ? p.v_scale[tile.y] : 1.f;
+                const float vs = F8 ? p.v_scale[run.y] : 1.f;
                 const int slot = 2 * worker + (begins ? 1 : 0);
 #pragma unroll
                 for (int r = 0; r < NT; ++r) {
@@ -769,9 +768,9 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
                 }
                 if (begins && !ends) {
                     // the worker of the unit's last tile, which is tiles - 1 - t behind this one
-                    const Span sp = span_of<KT>(p, tile.w);
-                    const long long rest = sp.tiles - 1 - (tile.z - sp.lo) / KT;
-                    const long long at = first + info.z + rest, split = longer * (share + 1);
+                    const Span sp = span_of<KT>(p, run.w);
+                    const long long rest = sp.tiles - 1 - (run.w - KT - dlo - sp.lo) / KT;
+                    const long long at = first + tile.w + rest, split = longer * (share + 1);
                     const int owner = int(at < split ? at / (share + 1) : longer + (at - split) / share);
                     rec = Rec{int64_t(n) * p.Hq + head0, heads, owner - worker};
                 }
@@ -784,7 +783,7 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
     } else {
         // ---- join the warps through their rings, which are free now
         cp_async_wait_group<0>();
-        const int n = cur.n;
+        const int n = cur.n, head0 = first_head(cur);
 #pragma unroll
         for (int r = 0; r < NT; ++r) {
             sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
@@ -1056,7 +1055,7 @@ inkling_status inkling_rel_attn_decode(const inkling_kv_cache_desc* cache, const
     p.token_stride = lay.token_stride * es;
     p.head_stride = lay.head_stride * es;
     const double scale = dims->scale > 0 ? dims->scale : 1.0 / std::sqrt(double(D));
-    p.scale_log2 = float(scale * 1.4426950408889634);
+    p.scale_log2 = std::max(float(scale * 1.4426950408889634), 0x1p-126f);
     p.q = q;
     p.k_cache = static_cast<const uint8_t*>(k_cache);
     p.v_cache = static_cast<const uint8_t*>(v_cache);

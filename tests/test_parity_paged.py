@@ -257,6 +257,17 @@ def test_decode_small_and_large_queries_e4m3():
     check(x, s, scale=2.0 ** -12)
 
 
+def test_decode_scales_that_underflow_leave_masked_keys_masked():
+    """A query of zeros with a tiny key scale, and a tiny logit scale: every logit is 0, and the keys
+    behind the length still do not count."""
+    x, s = problem([5, 33], 4, 1, 128, 16, 0, "e4m3", seed=23)
+    x["q"].zero_()
+    s["k_scale"].fill_(1e-30)
+    check(x, s)
+    y, t = problem([5, 33], 4, 1, 64, 16, 8, seed=24)
+    check(y, t, scale=1e-300)
+
+
 def test_decode_equal_calls_give_equal_bits():
     from learned_relative_gqa_b200 import binding
     x, s = problem([1500, 3, 700, 0], 16, 2, 128, 16, 64, seed=13)
