@@ -41,9 +41,10 @@
 // Measured (GPU time of a call, of the measured copy bandwidth): eight requests of 32767
 // tokens, 32 / 8 heads of 128, profiles of 4096: 177 us, 6.06 TB/s, 0.93; one of 32768: 30.9
 // us, 4.35 TB/s, 0.66 (of it 5 us until the first tile is in and 4 us for the join); 64
-// requests of 16 to 4096 tokens: 41.7 us, 4.74 TB/s, 0.72; 24 requests of 8191 to 32768
-// tokens in e4m3, 32 / 4 heads: 88 us, 5.2 TB/s, 0.80, bound by the instructions of a tile
-// (about 2,900 cycles for its 8 KB with two warps to a scheduler, no memory stalls).
+// requests of 16 to 4096 tokens: 41.9 us, 4.72 TB/s, 0.72; 24 requests of 8191 to 32768
+// tokens in e4m3, 32 / 4 heads: 87.3 us, 5.27 TB/s, 0.80, bound by the dependent
+// instructions of a tile (about 2,600 cycles for its 8 KB with two warps to a scheduler,
+// hardly any memory stalls).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -65,7 +66,11 @@ constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 320;
 constexpr int kMaxWorkers = kMaxCtas * kWarps;  // workspace slots: two per worker
 // One CTA per unit, with no split, up to these sizes: tiles of each of its warps, and units
-// of the call.
+// of the call. Both sides, GPU us whole / split, with 16 / 4 heads of 128 and requests of 1 to
+// 2048 tokens: window 512, 64 requests (4 warps, 8 tiles each) 12.2 / 14.1, 16 requests (8
+// warps, 4 tiles) 8.1 / 11.9; window 1024 (8 warps, 8 tiles) 1 request 11.2 / 9.4, 16
+// requests 11.2 / 11.8, 32 requests 13.0 / 12.6; window 512, 512 units 17.4 / 17.3, 800 units
+// 23.7 / 21.3.
 constexpr int kWholeTiles = 8;
 constexpr int kWholeUnits = 512;
 constexpr int kJoinThreads = 256;
@@ -159,6 +164,11 @@ struct Shape {
     static constexpr int RB = D * ES;                       // bytes of a row
     static constexpr int CPR = RB / 16;                     // 16-byte chunks of a row
     static constexpr int KT = (D == 128 && !F8) ? 16 : 32;  // keys of a tile
+    // e4m3: probabilities are taken 2^7 times, as FP16 has no exponent below 2^-24: so each of
+    // them is off by 2^-32 of the largest at most (they stay below 2^15, as the running
+    // maximum lags by 2^8 at most), and long tails of small ones are not lost.
+    static constexpr float LIFT = F8 ? 7.f : 0.f;
+    static_assert(kRescaleThreshold + LIFT <= 15.f, "FP16 ends below 2^16");
     static constexpr int STAGES = 3;
     static constexpr int SIDE = KT * RB;                    // bytes of K (or V) in a stage
     static constexpr int BCH = KT / 8 + 1;                  // 16-byte chunks that hold KT profile entries
@@ -667,7 +677,7 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
             uint32_t pr[TERMS][NT][NS];
 #pragma unroll
             for (int r = 0; r < NT; ++r) {
-                const float ref = mx[r] == -INFINITY ? 0.f : mx[r];
+                const float ref = mx[r] == -INFINITY ? 0.f : mx[r] - S::LIFT;
 #pragma unroll
                 for (int x = 0; x < NS; ++x) {
                     float p0 = ex2_approx(fmaf(s[x][2 * r], zs[r], -ref));
@@ -731,21 +741,22 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
 #pragma unroll
                 for (int r = 0; r < NT; ++r) {
                     const int h = g + 8 * r;
+                    const float m0 = mx[r] - S::LIFT;  // what the sum and O are relative to
                     float l = sum[r];
                     l += __shfl_xor_sync(0xffffffffu, l, 1);
                     l += __shfl_xor_sync(0xffffffffu, l, 2);
                     float mul = vs;
                     if (whole) {
-                        const float top = fmaxf(mx[r], qa.sink[r]);
-                        const float f = weight(mx[r], top);
+                        const float top = fmaxf(m0, qa.sink[r]);
+                        const float f = weight(m0, top);
                         const float tot = top == -INFINITY ? 0.f : l * f + weight(qa.sink[r], top);
                         mul = tot == 0.f ? 0.f : vs * f / tot;
                         if (t == 0 && h < heads) {
                             const int64_t at = int64_t(n) * p.Hq + head0 + h;
-                            p.lse[at] = lse_of(mx[r], top, tot, p.sink, at);
+                            p.lse[at] = lse_of(m0, top, tot, p.sink, at);
                         }
                     } else if (t == 0 && h < heads) {
-                        p.part_ml[int64_t(slot) * p.unit_heads + h] = make_float2(mx[r], l);
+                        p.part_ml[int64_t(slot) * p.unit_heads + h] = make_float2(m0, l);
                     }
                     float* const to = whole ? p.out + (int64_t(n) * p.Hq + head0 + 8 * r) * D
                                             : p.part_o + (int64_t(slot) * p.unit_heads + 8 * r) * D;
@@ -788,7 +799,7 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
         for (int r = 0; r < NT; ++r) {
             sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
             sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-            if (t == 0) s_ml[warp][g + 8 * r] = make_float2(mx[r], sum[r]);
+            if (t == 0) s_ml[warp][g + 8 * r] = make_float2(mx[r] - S::LIFT, sum[r]);
         }
         __syncwarp();
         float* const mine = reinterpret_cast<float*>(smem + warp * S::RING);
@@ -986,6 +997,7 @@ cudaError_t launch_decode(DecodeParams& p, cudaStream_t st) {
         if (r != cudaSuccess) return r;
         return launch_early(kernel, dim3(unsigned(grid)), 32 * warps, warps * S::RING, st, p);
     };
+    // eight warps where every unit has an SM to itself and more tiles than four warps
     if (unit_tiles <= 8 * kWholeTiles && unit_tiles > 4 && units <= sms) return launch(decode_kernel<S, 8>, units, 8);
     if (unit_tiles <= 4 * kWholeTiles && units <= kWholeUnits) return launch(decode_kernel<S, 4>, units, 4);
     const int64_t workers = std::max<int64_t>(units * (unit_tiles + 1) / S::MIN_TILES, 1);

@@ -55,7 +55,7 @@ def plan(old, new, table, free, count, page, max_tokens, num_pages):
 
 
 def decode(q, k, v, table, lens, profiles=None, sink=None, window=0, scale=None):
-    """out [N,Hq,D], lse [N,Hq] and, for error bounds, the largest scale * sum |q||k| and |z| of each row.
+    """out [N,Hq,D], lse [N,Hq] and, for error bounds, [N,Hq,2]: the largest scale * sum |q||k| and |z| of each row.
 
     ``k``, ``v`` are FP64 pools [pages, page, Hkv, D] (decoded and scaled)."""
     N, Hq, D = q.shape
@@ -63,7 +63,7 @@ def decode(q, k, v, table, lens, profiles=None, sink=None, window=0, scale=None)
     M = table.shape[1]
     scale = D ** -0.5 if scale is None else scale
     out, lse = np.zeros((N, Hq, D)), np.full((N, Hq), -np.inf)
-    mag = np.zeros((N, Hq))
+    mag = np.zeros((N, Hq, 2))
     for n in range(N):
         L = min(max(int(lens[n]), 0), M * page)
         js = [j for j in range(max(0, L - window) if window else 0, L) if 0 <= table[n, j // page] < pages]
@@ -82,7 +82,7 @@ def decode(q, k, v, table, lens, profiles=None, sink=None, window=0, scale=None)
                 R = profiles.shape[2]
                 z = z + np.where(d < R, profiles[n, h][np.minimum(d, R - 1)], 0.0)
             finite = np.isfinite(z)
-            mag[n, h] = (scale * (np.abs(kk) @ np.abs(q[n, h]))).max() + np.abs(z[finite]).max(initial=0.0)
+            mag[n, h] = (scale * (np.abs(kk) @ np.abs(q[n, h]))).max(), np.abs(z[finite]).max(initial=0.0)
             top = max(z.max(), sk)
             if top == -np.inf:
                 continue

@@ -3,8 +3,8 @@ where they can go wrong.
 
 Tolerances of the attention, per row, from the arithmetic (u = 2^-24, half an FP32 step):
 * a logit: D products summed in FP32, dz = (D + 16) u sum|q||k| scale + 4 u |z|
-  (``mag`` of the oracle bounds both sums; the factor 4 covers the products with the scale
-  and log2 e and the bias, one rounding each);
+  (``mag`` of the oracle holds both; the factor 4 covers the products with the scale and
+  log2 e and the bias, one rounding each);
 * a probability: 2 dz relative (value and maximum), the exponential's 2^-22, and in the
   second product its two-part form, off by at most 2^-8 of 2^-8 of it (BF16; FP16 is finer);
 * sums over the keys: a lane adds a sixteenth of a part's keys one after the other, and
@@ -108,7 +108,7 @@ def check(x, scales, window=0, scale=None, got=None):
     o_ref, l_ref, mag = ref.decode(f64(x["q"]), k, v, x["block_table"].cpu().numpy(), x["lens"].cpu().numpy(),
                                    f64(x["profiles"]), f64(x["sink"]), window, scale)
     D, L = x["q"].shape[2], max(1, int(x["lens"].max()))
-    dz = (D + 16) * U * mag + 4 * U * mag
+    dz = (D + 16) * U * mag[:, :, 0] + 4 * U * mag[:, :, 1]
     vmax = np.nanmax(np.abs(v)) if np.isfinite(v).any() else 0.0
     o_tol = vmax * (2.0 ** -16 + 2 * (2 * dz + 2.0 ** -22) + 2 * (L / 8 + 64) * U)
     finite = np.isfinite(l_ref)
@@ -266,6 +266,20 @@ def test_decode_scales_that_underflow_leave_masked_keys_masked():
     check(x, s)
     y, t = problem([5, 33], 4, 1, 64, 16, 8, seed=24)
     check(y, t, scale=1e-300)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_decode_keeps_a_long_tail_of_small_probabilities(dtype):
+    """One key with probability 1 and 5999 with e^-17.375 = 2^-25.07 of it each, all with the largest
+    value: together they are 1.7e-4 of the result."""
+    for lens in ([6000], [400], [6000, 5, 900]):
+        x, s = problem(lens, 8, 1, 128, 64, 6000, dtype, seed=25, poison=False)
+        x["q"].zero_()
+        x["profiles"].fill_(-17.375)
+        x["profiles"][:, :, 0] = 0
+        x["sink"].fill_(-30.0)
+        x["v_cache"].copy_(torch.full(x["v_cache"].shape, 448.0 if dtype == "e4m3" else 3.0, device="cuda"))
+        check(x, s)
 
 
 def test_decode_equal_calls_give_equal_bits():
