@@ -4,7 +4,9 @@ Argument marshalling only: every step of the attention runs in the library's
 CUDA kernels. The functions carry the C entry points' names; tensors are
 PyTorch device tensors (PyTorch supplies device memory and streams), passed
 to the library as raw pointers. There is no fallback: if the library is
-missing or fails to load, every call raises.
+missing or fails to load, every call raises. The serving calls (``kv_plan``,
+``kv_append``, ``paged_decode``) marshal in a native module, ``_serving``, as
+they take a few microseconds on the GPU.
 """
 from __future__ import annotations
 
