@@ -484,20 +484,20 @@ def l2clip_backward(x, dy, threshold: float, scale=None, tau=None, stream=None):
 # --------------------------------------------------------------------------
 # serving: paged key-value cache and single-token attention (include/inkling_paged_attn.h)
 # --------------------------------------------------------------------------
-_bound = None
+_ext = _bound = None
 
 
 def _serving():
     """The `_serving` extension (csrc/serving_ext.cpp), calling the loaded library."""
-    global _bound
-    lib = load()
-    from . import _serving as ext
-    if _bound is not lib:
+    global _ext, _bound
+    if _bound is None or _bound is not _lib:
+        lib = load()
+        from . import _serving as ext
         ext.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.inkling_kv_plan, lib.inkling_kv_append, lib.inkling_rel_attn_decode,
             lib.inkling_rel_attn_decode_workspace_size)))
-        _bound = lib
-    return ext
+        _ext, _bound = ext, lib
+    return _ext
 
 
 def _current(stream, device):

@@ -960,6 +960,23 @@ Layout layout_of(int64_t D, int64_t group) {
     return l;
 }
 
+// Query heads of a unit are 8 or 16, a tile's keys 16 or 32 (Shape).
+int64_t units_of(int64_t requests, int64_t heads_kv, int64_t group) {
+    return requests * heads_kv * (group <= 8 ? 1 : (group + 15) / 16);
+}
+int64_t tiles_of(int64_t span, int64_t head_dim, bool e4m3) {
+    const int64_t kt = head_dim == 128 && !e4m3 ? 16 : 32;
+    return (span + kt - 1) / kt;
+}
+
+// Sizes that take the whole form on any device: no workspace is used.
+bool never_split(const inkling_kv_cache_desc* c, const inkling_rel_attn_decode_dims* d) {
+    int64_t span = d->max_pages * c->page_size;
+    if (d->window > 0 && d->window < span) span = d->window;
+    return tiles_of(span, c->head_dim, c->dtype == INKLING_KV_E4M3) <= 4 * kWholeTiles &&
+           units_of(d->requests, c->heads_kv, d->heads_q / c->heads_kv) <= kWholeUnits;
+}
+
 inkling_status check_decode(const inkling_kv_cache_desc* c, const inkling_rel_attn_decode_dims* d, CacheLayout* lay) {
     const inkling_status s = check_cache(c, lay);
     if (s != INKLING_OK) return s;
@@ -983,14 +1000,15 @@ template <class S>
 cudaError_t launch_decode(DecodeParams& p, cudaStream_t st) {
     p.hblocks = (p.group + 8 * S::NT - 1) / (8 * S::NT);
     p.unit_heads = p.group < 8 * S::NT ? p.group : 8 * S::NT;
+    static_assert(S::KT == (S::D == 128 && !S::F8 ? 16 : 32), "tiles_of");
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     // at most the tiles of a full table
     const int span = p.W > 0 && p.W < p.cap ? p.W : p.cap;
-    const int64_t unit_tiles = (span + S::KT - 1) / S::KT;
-    const int64_t units = int64_t(p.N) * p.Hkv * p.hblocks;
+    const int64_t unit_tiles = tiles_of(span, S::D, S::F8);
+    const int64_t units = units_of(p.N, p.Hkv, p.group);
     auto launch = [&](auto kernel, int64_t grid, int warps) {
         cudaError_t r =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, warps * S::RING);
@@ -1026,6 +1044,7 @@ size_t inkling_rel_attn_decode_workspace_size(const inkling_kv_cache_desc* cache
                                               const inkling_rel_attn_decode_dims* dims) {
     CacheLayout lay;
     if (check_decode(cache, dims, &lay) != INKLING_OK) return 0;
+    if (never_split(cache, dims)) return 256;
     return layout_of(cache->head_dim, dims->heads_q / cache->heads_kv).total;
 }
 
@@ -1049,7 +1068,7 @@ inkling_status inkling_rel_attn_decode(const inkling_kv_cache_desc* cache, const
         return INKLING_ERR_INVALID_ARG;
     const int64_t D = cache->head_dim;
     const Layout l = layout_of(D, dims->heads_q / cache->heads_kv);
-    if (workspace_bytes < l.total) return INKLING_ERR_INVALID_ARG;
+    if (workspace_bytes < (never_split(cache, dims) ? 256 : l.total)) return INKLING_ERR_INVALID_ARG;
 
     DecodeParams p{};
     p.N = int(dims->requests);

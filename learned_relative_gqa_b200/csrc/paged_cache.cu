@@ -223,7 +223,7 @@ struct AppendParams {
     void* v_cache;
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -281,7 +281,9 @@ constexpr int kPerLane = E4M3 ? 16 : 8;
 // (e4m3) bytes per value, bound by HBM; e4m3 by its arithmetic too (77 % of the issue slots
 // with 8 values to a lane, which is why a lane has 16). No loop, so that a full SM keeps
 // 2048 threads' loads in flight. The clip's sum of squares is FP32 over the group by shuffles.
-// 32768 clipped rows of 8 x 128: 42.0 us, 6.40 TB/s; one step of 64 rows: 1.6 us.
+// 32768 clipped rows of 8 x 128: 41.8 us, 6.43 TB/s; 16381 clipped rows of 4 x 128 to e4m3
+// 11.4 us, 4.4 TB/s; one step of 64 rows: 1.3 us. (128 threads to a block: with 256, 11.6 and
+// 1.5 us; held to fewer registers, the e4m3 form spills and takes 12.9 us and more.)
 template <int D, bool E4M3, bool CLIP>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int PER = kPerLane<E4M3>, LPR = D / PER;

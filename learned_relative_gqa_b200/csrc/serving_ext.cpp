@@ -248,17 +248,20 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (ws) check(ws, "workspace", dev, at::kByte, {ws->numel()});
     const inkling_rel_attn_decode_dims dims{N, Hq, R, integer(a[7]), M, a[8] == Py_None ? 0.0 : real(a[8])};
     const c10::cuda::CUDAGuard guard(dev);
-    at::Tensor own;
-    if (!ws) {
-        const size_t size = g_decode_size(&cache, &dims);
-        if (size != 0) own = at::empty({int64_t(size)}, at::TensorOptions().dtype(at::kByte).device(dev));
-        ws = &own;
-    }
     Outputs outs;
     outs.add(at::kFloat, {N, Hq, D});
     outs.add(at::kFloat, {N, Hq});
+    // a workspace of its own, so that it can be used again when the call returns; a small one
+    // (the sizes that need none) costs less beside the outputs
+    at::Tensor own;
+    const size_t size = ws ? 0 : g_decode_size(&cache, &dims);
+    const bool beside = size != 0 && size <= 256;
+    if (beside) outs.add(at::kByte, {int64_t(size)});
+    else if (size != 0) own = at::empty({int64_t(size)}, at::TensorOptions().dtype(at::kByte).device(dev));
     outs.allocate(dev);
     const at::Tensor out = outs.get(0), lse = outs.get(1);
+    if (beside) own = outs.get(2);
+    if (!ws) ws = &own;
     const inkling_status s = g_decode(
         &cache, &dims, data<uint16_t>(&q), kc.data_ptr(), vc.data_ptr(), data<float>(ks), data<float>(vs),
         R ? data<uint16_t>(prof) : nullptr, data<float>(sink), data<int32_t>(&table), data<int32_t>(&lens),
