@@ -492,7 +492,11 @@ def _serving():
     global _ext, _bound
     if _bound is None or _bound is not _lib:
         lib = load()
-        from . import _serving as ext
+        try:
+            from . import _serving as ext
+        except ImportError as e:
+            raise RuntimeError("_serving.so is not built for this interpreter and PyTorch; "
+                               "run python -m learned_relative_gqa_b200.build") from e
         ext.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.inkling_kv_plan, lib.inkling_kv_append, lib.inkling_rel_attn_decode,
             lib.inkling_rel_attn_decode_workspace_size)))
