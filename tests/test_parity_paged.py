@@ -150,6 +150,28 @@ def test_decode(lens, hq, hkv, d, page, r, window, dtype, layout):
             assert not out[n].any() and np.array_equal(lse[n], f64(x["sink"])[n])
 
 
+def random_case(seed):
+    rng = np.random.default_rng(seed)
+    hkv = int(rng.choice([1, 2, 3, 5]))
+    group = int(rng.choice([1, 2, 3, 4, 7, 8, 9, 16, 17]))
+    n = int(rng.choice([1, 2, 5, 17, 40]))
+    most = int(rng.choice([40, 300, 1500 if n < 10 else 300]))
+    lens = [int(x) if rng.random() < 0.9 else 0 for x in rng.integers(1, most + 1, n)]
+    page = int(rng.choice([1, 3, 8, 16, 17, 24, 32, 40, 64, 500, 2048]))
+    return dict(lens=lens, hq=hkv * group, hkv=hkv, d=int(rng.choice([64, 128])), page=page,
+                r=8 * int(rng.choice([0, 1, 5, 40, 300])), dtype=str(rng.choice(["bf16", "e4m3"])),
+                layout=str(rng.choice(["nhd", "hnd"])), seed=seed,
+                max_pages=max(1, -(-max(lens + [1]) // page)) + int(rng.choice([0, 3, 2000 // page + 1])),
+                sink=bool(rng.random() < 0.8)), int(rng.choice([0, 0, 1, 7, 64, 200]))
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_decode_random_shapes(seed):
+    kw, window = random_case(seed)
+    x, s = problem(**kw)
+    check(x, s, window)
+
+
 @pytest.mark.parametrize("hq,hkv,d,dtype", [(16, 1, 128, "bf16"), (16, 1, 64, "e4m3"), (4, 2, 128, "e4m3"),
                                             (40, 2, 64, "bf16")])
 @pytest.mark.parametrize("lens", [[0], [1], [0, 0, 1], [5, 0, 40, 1, 1, 0, 2], [33] * 40])
