@@ -6,7 +6,8 @@
  *
  * A serving step is three calls, each asynchronous on `stream`, none of which
  * needs the lengths or the tables on the host (so a step can be captured in a
- * CUDA graph and replayed):
+ * CUDA graph and replayed). Nothing is kept between calls but, per device, its number
+ * of SMs and whether a kernel's shared-memory limit has been raised:
  *   inkling_kv_plan          pages of the growing requests, slots of the new tokens
  *   inkling_kv_append        new key / value rows into their slots (k clipped, 8 bits)
  *   inkling_rel_attn_decode  attention of each request's last token

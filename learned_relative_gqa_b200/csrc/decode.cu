@@ -46,6 +46,7 @@
 // take about 2,600 cycles for its 8 KB with two warps to a scheduler, which is what HBM
 // takes as well). A plain sum over as many bytes takes 181, 29.0, 38.3 and 89.4 us.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -996,6 +997,36 @@ inkling_status check_decode(const inkling_kv_cache_desc* c, const inkling_rel_at
 
 inkling_status status_of(cudaError_t e) { return note_cuda_error(e) == cudaSuccess ? INKLING_OK : INKLING_ERR_CUDA; }
 
+// Streaming multiprocessors of a device, looked up once.
+cudaError_t sm_count(int dev, int* sms) {
+    static std::atomic<int> known[64];
+    *sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (*sms != 0) return cudaSuccess;
+    const cudaError_t e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+    return e;
+}
+
+// The kernel's limit of dynamic shared memory is raised on a device's first launch, and again
+// where a launch finds it too low (the device was reset since).
+template <class S, int WHOLE>
+cudaError_t launch_form(const DecodeParams& p, int64_t grid, int dev, cudaStream_t st) {
+    constexpr int warps = WHOLE ? WHOLE : kWarps;
+    static std::atomic<uint64_t> raised{0};
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    for (bool again = false;; again = true) {
+        if (again || !(raised.load(std::memory_order_relaxed) & bit)) {
+            const cudaError_t e = cudaFuncSetAttribute(decode_kernel<S, WHOLE>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, warps * S::RING);
+            if (e != cudaSuccess) return e;
+            raised.fetch_or(bit, std::memory_order_relaxed);
+        }
+        const cudaError_t e =
+            launch_early(decode_kernel<S, WHOLE>, dim3(unsigned(grid)), 32 * warps, warps * S::RING, st, p);
+        if (e != cudaErrorInvalidValue || again) return e;
+    }
+}
+
 template <class S>
 cudaError_t launch_decode(DecodeParams& p, cudaStream_t st) {
     p.hblocks = (p.group + 8 * S::NT - 1) / (8 * S::NT);
@@ -1003,26 +1034,20 @@ cudaError_t launch_decode(DecodeParams& p, cudaStream_t st) {
     static_assert(S::KT == (S::D == 128 && !S::F8 ? 16 : 32), "tiles_of");
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = sm_count(dev, &sms);
     if (e != cudaSuccess) return e;
     // at most the tiles of a full table
     const int span = p.W > 0 && p.W < p.cap ? p.W : p.cap;
     const int64_t unit_tiles = tiles_of(span, S::D, S::F8);
     const int64_t units = units_of(p.N, p.Hkv, p.group);
-    auto launch = [&](auto kernel, int64_t grid, int warps) {
-        cudaError_t r =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, warps * S::RING);
-        if (r != cudaSuccess) return r;
-        return launch_early(kernel, dim3(unsigned(grid)), 32 * warps, warps * S::RING, st, p);
-    };
     // eight warps where every unit has an SM to itself and more tiles than four warps
-    if (unit_tiles <= 8 * kWholeTiles && unit_tiles > 4 && units <= sms) return launch(decode_kernel<S, 8>, units, 8);
-    if (unit_tiles <= 4 * kWholeTiles && units <= kWholeUnits) return launch(decode_kernel<S, 4>, units, 4);
+    if (unit_tiles <= 8 * kWholeTiles && unit_tiles > 4 && units <= sms) return launch_form<S, 8>(p, units, dev, st);
+    if (unit_tiles <= 4 * kWholeTiles && units <= kWholeUnits) return launch_form<S, 4>(p, units, dev, st);
     const int64_t workers = std::max<int64_t>(units * (unit_tiles + 1) / S::MIN_TILES, 1);
     int64_t grid = int64_t(sms) * kCtasPerSm;
     if (grid > kMaxCtas) grid = kMaxCtas;
     if (grid > (workers + kWarps - 1) / kWarps) grid = (workers + kWarps - 1) / kWarps;
-    e = launch(decode_kernel<S, 0>, grid, kWarps);
+    e = launch_form<S, 0>(p, grid, dev, st);
     if (e != cudaSuccess) return e;
     return launch_early(decode_join_kernel<S::D>,
                         dim3(unsigned((grid * kWarps + 31) / 32), unsigned(p.unit_heads), 4), kJoinThreads, 0, st, p,

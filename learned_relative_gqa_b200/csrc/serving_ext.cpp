@@ -12,6 +12,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -116,13 +117,16 @@ class Outputs {
         it.at = bytes_;
         bytes_ += (n + 255) / 256 * 256;
     }
-    void allocate(at::Device dev) {
-        whole_ = at::empty({bytes_}, at::TensorOptions().dtype(at::kByte).device(dev));
+    // on the current device and stream
+    void allocate() {
+        c10::Allocator* const allocator = c10::cuda::CUDACachingAllocator::get();
+        whole_ = c10::Storage(c10::Storage::use_byte_size_t(), size_t(bytes_), allocator->allocate(size_t(bytes_)),
+                              allocator, /*resizable=*/false);
     }
     at::Tensor get(int i) const {
         const Item& it = items_[i];
-        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole_.storage()), whole_.key_set(),
-                                                                c10::scalarTypeToTypeMeta(it.type));
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+            c10::Storage(whole_), c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(it.type));
         t.unsafeGetTensorImpl()->set_storage_offset(it.at / int64_t(c10::elementSize(it.type)));
         t.unsafeGetTensorImpl()->set_sizes_contiguous(c10::IntArrayRef(it.sizes, it.dims));
         return t;
@@ -138,7 +142,7 @@ class Outputs {
     Item items_[kMost];
     int count_ = 0;
     int64_t bytes_ = 0;
-    at::Tensor whole_;
+    c10::Storage whole_;
 };
 
 PyObject* status(inkling_status s) { return PyLong_FromLong(s); }
@@ -171,7 +175,7 @@ PyObject* kv_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     outs.add(at::kInt, {N + 1});
     if (!lens_out) outs.add(at::kInt, {N});
     if (!info_out) outs.add(at::kInt, {4});
-    outs.allocate(dev);
+    outs.allocate();
     const at::Tensor slots = outs.get(0), positions = outs.get(1), start = outs.get(2);
     const at::Tensor lens = lens_out ? *lens_out : outs.get(3), info = info_out ? *info_out : outs.get(lens_out ? 3 : 4);
     const inkling_kv_plan_dims dims{N, page_size, M, num_pages, T};
@@ -180,9 +184,23 @@ PyObject* kv_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
                data<int32_t>(&count), data<int32_t>(&lens), data<int32_t>(&start), data<int64_t>(&slots),
                data<int32_t>(&positions), data<int32_t>(&info), c10::cuda::getCurrentCUDAStream(dev.index()).stream());
     if (s != INKLING_OK) return status(s);
-    return Py_BuildValue("{s:N,s:N,s:N,s:N,s:N}", "lens", THPVariable_Wrap(lens), "query_start",
-                         THPVariable_Wrap(start), "slots", THPVariable_Wrap(slots), "positions",
-                         THPVariable_Wrap(positions), "info", THPVariable_Wrap(info));
+    PyObject* const d = PyDict_New();
+    if (!d) return nullptr;
+    static PyObject* const names[] = {
+        PyUnicode_InternFromString("lens"), PyUnicode_InternFromString("query_start"),
+        PyUnicode_InternFromString("slots"), PyUnicode_InternFromString("positions"),
+        PyUnicode_InternFromString("info")};
+    const at::Tensor* const values[] = {&lens, &start, &slots, &positions, &info};
+    for (int i = 0; i < 5; ++i) {
+        PyObject* const v = THPVariable_Wrap(*values[i]);
+        const bool set = v && names[i] && PyDict_SetItem(d, names[i], v) == 0;
+        Py_XDECREF(v);
+        if (!set) {
+            Py_DECREF(d);
+            return nullptr;
+        }
+    }
+    return d;
     END_HANDLE_TH_ERRORS
 }
 
@@ -253,15 +271,16 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     outs.add(at::kFloat, {N, Hq});
     // a workspace of its own, so that it can be used again when the call returns; a small one
     // (the sizes that need none) costs less beside the outputs
-    at::Tensor own;
+    Outputs own;
     const size_t size = ws ? 0 : g_decode_size(&cache, &dims);
-    const bool beside = size != 0 && size <= 256;
-    if (beside) outs.add(at::kByte, {int64_t(size)});
-    else if (size != 0) own = at::empty({int64_t(size)}, at::TensorOptions().dtype(at::kByte).device(dev));
-    outs.allocate(dev);
+    Outputs& home = size <= 256 ? outs : own;
+    if (size != 0) home.add(at::kByte, {int64_t(size)});
+    outs.allocate();
     const at::Tensor out = outs.get(0), lse = outs.get(1);
-    if (beside) own = outs.get(2);
-    if (!ws) ws = &own;
+    if (size > 256) own.allocate();
+    at::Tensor scratch;
+    if (size != 0) scratch = home.get(size <= 256 ? 2 : 0);
+    if (!ws) ws = &scratch;
     const inkling_status s = g_decode(
         &cache, &dims, data<uint16_t>(&q), kc.data_ptr(), vc.data_ptr(), data<float>(ks), data<float>(vs),
         R ? data<uint16_t>(prof) : nullptr, data<float>(sink), data<int32_t>(&table), data<int32_t>(&lens),
