@@ -35,6 +35,7 @@ struct PlanParams {
 };
 
 constexpr int kPlanThreads = 1024;
+constexpr size_t kPlanStatic = 32 * sizeof(int3);  // shared memory of plan_kernel beside the prefix sums
 
 __device__ __forceinline__ int pages_of(int len, const PageDivisor& page) {
     return len > 0 ? page.index(len - 1) + 1 : 0;
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     int* s_tok = s_at;               // [N + 1] exclusive prefix sums, totals at [N]
     int* s_need = s_tok + p.N + 1;
     int* s_back = s_need + p.N + 1;
-    __shared__ int3 s_warp[32];
+    __shared__ int3 s_warp[kPlanStatic / sizeof(int3)];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // no early release: blocks of a successor that come in beside these share their SMs unevenly
     // (two plans of 4096 requests in a row 13.5 us each instead of 9.0)
@@ -433,7 +434,7 @@ inkling_status inkling_kv_plan(const inkling_kv_plan_dims* dims, const int32_t* 
     PlanParams p{int(N), int(dims->max_pages), int(dims->num_pages), int(T), PageDivisor(dims->page_size),
                  old_lens, new_lens, block_table, free_pages, free_count, lens, query_start, slots, positions, info};
     const size_t smem = (N + 1) * 12;
-    if (smem > 48 * 1024) {
+    if (smem + kPlanStatic > 48 * 1024) {  // what a launch gets without asking holds both
         const cudaError_t e =
             cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return status_of(e);
