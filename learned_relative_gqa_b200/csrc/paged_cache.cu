@@ -35,6 +35,7 @@ struct PlanParams {
 };
 
 constexpr int kPlanThreads = 1024;
+constexpr int64_t kPlanMaxRequests = 16384;
 constexpr size_t kPlanStatic = 32 * sizeof(int3);  // shared memory of plan_kernel beside the prefix sums
 
 __device__ __forceinline__ int pages_of(int len, const PageDivisor& page) {
@@ -191,7 +192,7 @@ inkling_status check_plan(const inkling_kv_plan_dims* d) {
     if (d->requests < 0 || d->page_size <= 0 || d->max_pages <= 0 || d->num_pages <= 0 || d->max_tokens < 0)
         return INKLING_ERR_INVALID_ARG;
     const int64_t lim = int64_t(1) << 30;
-    if (d->requests > 16384 || d->page_size >= lim || d->max_pages >= lim || d->num_pages > 0x7fffffff ||
+    if (d->requests > kPlanMaxRequests || d->page_size >= lim || d->max_pages >= lim || d->num_pages > 0x7fffffff ||
         d->max_tokens > lim)
         return INKLING_ERR_UNSUPPORTED;
     const int64_t cap = d->max_pages * d->page_size;
@@ -435,8 +436,10 @@ inkling_status inkling_kv_plan(const inkling_kv_plan_dims* dims, const int32_t* 
                  old_lens, new_lens, block_table, free_pages, free_count, lens, query_start, slots, positions, info};
     const size_t smem = (N + 1) * 12;
     if (smem + kPlanStatic > 48 * 1024) {  // what a launch gets without asking holds both
-        const cudaError_t e =
-            cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        // always to the largest batch's size: a thread that set its own would take the limit from
+        // under another one's launch
+        const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   int((kPlanMaxRequests + 1) * 12));
         if (e != cudaSuccess) return status_of(e);
     }
     // At most one block per SM: more would only repeat the prefix sums. The pages taken and

@@ -1,5 +1,6 @@
 """The page plan at the sizes where its shared memory passes what a launch gets without asking, and
 called by several host threads at once."""
+import ctypes
 import os
 import subprocess
 import sys
@@ -63,3 +64,64 @@ def test_plan_at_the_limit_of_a_launch(sizes):
     code = f"import sys; sys.path.insert(0, {ROOT!r}); from tests import test_paged_plan_limits as t; t.plans({sizes!r})"
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_plans_of_different_sizes_in_one_graph():
+    from learned_relative_gqa_b200 import binding
+    cases = [step(N) for N in (16384, 5000, 64)]
+    saved = [(x["block_table"].clone(), x["free_pages"].clone()) for x, _, _ in cases]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [binding.kv_plan(**x, **kw) for x, kw, _ in cases]
+    for _ in range(2):
+        for (x, _, _), (table, free) in zip(cases, saved):
+            x["block_table"].copy_(table)
+            x["free_pages"].copy_(free)
+        graph.replay()
+        for g, (x, _, want) in zip(got, cases):
+            same(g, x, want)
+
+
+def test_plans_of_different_sizes_from_two_threads():
+    """Two host threads with a stream and buffers each, one with the largest batch and one with a smaller:
+    neither may take the other's shared-memory limit away."""
+    from learned_relative_gqa_b200 import binding as B
+    fails, ready = [], threading.Barrier(2)
+
+    def work(N):
+        try:
+            x, kw, want = step(N)
+            T, M = kw["max_tokens"], x["block_table"].shape[1]
+            i32 = dict(dtype=torch.int32, device="cuda")
+            out = dict(lens=torch.empty(N, **i32), query_start=torch.empty(N + 1, **i32),
+                       slots=torch.empty(T, dtype=torch.int64, device="cuda"), positions=torch.empty(T, **i32),
+                       info=torch.empty(4, **i32))
+            dims = B.KVPlanDims(N, kw["page_size"], M, kw["num_pages"], T)
+            st = torch.cuda.Stream()
+            first = {n: x[n].clone() for n in ("block_table", "free_pages")}
+            st.wait_stream(torch.cuda.current_stream())
+            ready.wait(60)
+            # with its arguments made once, so that the threads are inside the library most of the time
+            # (repeated plans write the same entries)
+            ptr = [ctypes.c_void_p(t.data_ptr()) for t in (*x.values(), *out.values())]
+            call, args = B.load().inkling_kv_plan, (ctypes.byref(dims), *ptr, ctypes.c_void_p(st.cuda_stream))
+            for _ in range(20000):
+                status = call(*args)
+                if status != B.INKLING_OK:
+                    raise B.InklingError(status, "inkling_kv_plan")
+            st.synchronize()
+            with torch.cuda.stream(st):
+                for n, t in first.items():
+                    x[n].copy_(t)
+                B.inkling_kv_plan(dims, *x.values(), *out.values(), st)
+                st.synchronize()
+                same(out, x, want)
+        except Exception as e:  # noqa: BLE001
+            fails.append((N, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(N,)) for N in (16384, 5000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not fails, fails
