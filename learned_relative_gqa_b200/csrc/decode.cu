@@ -643,7 +643,9 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
                             if (!((mask >> (8 * x + 2 * t + e)) & 1u)) s[x][2 * r + e] = -INFINITY;
             }
             // ---- the running maximum moves only when a logit passes it by 2^8, which each lane
-            // sees for its own entries: no exchange in the usual tile
+            // sees for its own entries: no exchange in the usual tile. Compared as the exponents
+            // are taken below, from the lifted maximum: at 2^24 and above that is rounded by as
+            // much as 4, and a probability must still fit into FP16.
             float top[NT];
             bool grows = false;
 #pragma unroll
@@ -652,7 +654,7 @@ __global__ void __launch_bounds__(32 * (WHOLE ? WHOLE : kWarps), WHOLE == 8 ? 1 
 #pragma unroll
                 for (int x = 0; x < NS; ++x) top[r] = fmax3(top[r], s[x][2 * r], s[x][2 * r + 1]);
                 top[r] *= zs[r];
-                grows |= top[r] > mx[r] + kRescaleThreshold;
+                grows |= top[r] - (mx[r] - S::LIFT) > kRescaleThreshold + S::LIFT;
             }
             if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
