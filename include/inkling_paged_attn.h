@@ -86,8 +86,9 @@ typedef struct {
  * beyond T have no entry. Table entries other than the new pages, and entries of
  * free_pages at or above the new count, stay as they were. Lengths outside
  * [0, M * P] and a count outside [0, num_pages] are taken as the nearest bound; the
- * slots of tokens whose page number is outside the pool are -1. The outputs
- * (lens, query_start, slots, positions, info) may not overlap the inputs.
+ * slots of tokens whose page number is outside the pool are -1. What is written
+ * (block_table, free_pages, lens, query_start, slots, positions, info) may not
+ * overlap anything else (INKLING_ERR_INVALID_ARG).
  * slots needs 8-byte alignment, the rest 4.
  */
 inkling_status inkling_kv_plan(const inkling_kv_plan_dims* dims, const int32_t* old_lens, const int32_t* new_lens,

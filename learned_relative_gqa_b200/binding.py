@@ -580,7 +580,7 @@ def kv_plan(old_lens, new_lens, block_table, free_pages, free_count, *, page_siz
     ``slots`` [max_tokens] int64, ``positions`` [max_tokens] and ``info`` [4] (pages free
     afterwards, new tokens, pages short, pages taken). ``info[:1]`` is the next call's
     ``free_count`` (see include/inkling_paged_attn.h). ``lens`` and ``info`` may be given,
-    to be written; they may not overlap an input.
+    to be written; they may not overlap an input or each other.
     """
     if stream is not None:
         with _current(stream, block_table.device):

@@ -429,16 +429,15 @@ inkling_status inkling_kv_plan(const inkling_kv_plan_dims* dims, const int32_t* 
                           static_cast<const void*>(info)})
         if (!aligned(q, 4)) return INKLING_ERR_INVALID_ARG;
     if (!aligned(slots, 8)) return INKLING_ERR_INVALID_ARG;
-    const struct { const void* p; size_t n; } in[] = {
-        {old_lens, N * 4}, {new_lens, N * 4}, {block_table, N * size_t(dims->max_pages) * 4},
-        {free_pages, size_t(dims->num_pages) * 4}, {free_count, 4}};
-    const struct { const void* p; size_t n; } outs[] = {
-        {lens, N * 4}, {query_start, (N + 1) * 4}, {slots, T * 8}, {positions, T * 4}, {info, 16}};
-    for (const auto& o : outs)
-        for (const auto& i : in)
-            if (overlap(o.p, o.n, i.p, i.n)) return INKLING_ERR_INVALID_ARG;
-    if (overlap(block_table, N * size_t(dims->max_pages) * 4, free_pages, size_t(dims->num_pages) * 4))
-        return INKLING_ERR_INVALID_ARG;
+    // what is written may be read or written nowhere else: the blocks do not wait for each other
+    constexpr int kWritten = 7, kBuffers = 10;
+    const struct { const void* p; size_t n; } buffers[kBuffers] = {
+        {block_table, N * size_t(dims->max_pages) * 4}, {free_pages, size_t(dims->num_pages) * 4}, {lens, N * 4},
+        {query_start, (N + 1) * 4}, {slots, T * 8}, {positions, T * 4}, {info, 16},
+        {old_lens, N * 4}, {new_lens, N * 4}, {free_count, 4}};
+    for (int i = 0; i < kWritten; ++i)
+        for (int j = i + 1; j < kBuffers; ++j)
+            if (overlap(buffers[i].p, buffers[i].n, buffers[j].p, buffers[j].n)) return INKLING_ERR_INVALID_ARG;
 
     PlanParams p{int(N), int(dims->max_pages), int(dims->num_pages), int(T), PageDivisor(dims->page_size),
                  old_lens, new_lens, block_table, free_pages, free_count, lens, query_start, slots, positions, info};
