@@ -7,6 +7,7 @@ The library is written next to this file; nothing is installed elsewhere.
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 
@@ -41,7 +42,13 @@ def stale(path: str = LIB_PATH) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-_stale = stale
+def ext_unavailable() -> str:
+    """Why the Python module cannot be built on this machine; empty where it can."""
+    try:
+        import torch  # noqa: F401
+    except ImportError as e:
+        return f"PyTorch cannot be imported ({e})"
+    return "" if shutil.which("g++") else "there is no g++"
 
 
 def ext_command(out_path: str) -> list:
@@ -61,34 +68,45 @@ def ext_command(out_path: str) -> list:
 
 
 def build(force: bool = False, verbose: bool = False, out_path: str = LIB_PATH, defines: tuple = ()) -> str:
-    """Compile the library. ``defines`` / ``out_path`` build diagnostic variants
-    (for example ``INKLING_TRACE``) next to, not over, the product library."""
-    if not force and not defines and out_path == LIB_PATH and not _stale() and not stale(EXT_PATH):
-        return LIB_PATH
-    objs = []
-    build_dir = os.path.join(ROOT, "_build", "-".join(defines) or "default")
-    os.makedirs(build_dir, exist_ok=True)
-    common = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", CSRC, "-I", INCLUDE,
-              "--expt-relaxed-constexpr"]
-    if verbose:
-        common += ["-Xptxas", "-v"]
-    common += [f"-D{d}" for d in defines]
-    procs = []
-    for src in SOURCES:  # translation units compile side by side
-        obj = os.path.join(build_dir, src.replace(".cu", ".o"))
-        procs.append((subprocess.Popen(common + ["-c", os.path.join(CSRC, src), "-o", obj]), src))
-        objs.append(obj)
+    """Compile the library and, with it, the Python module. ``defines`` / ``out_path`` build diagnostic
+    variants of the library (for example ``INKLING_TRACE``) next to, not over, the product one.
+
+    The library needs neither PyTorch nor the module: it is built without them too, and the serving
+    calls of ``binding`` then say that the module is missing."""
     product = out_path == LIB_PATH and not defines
-    if product:
-        procs.append((subprocess.Popen(ext_command(EXT_PATH + ".tmp")), os.path.basename(EXT_SOURCE)))
+    due = force or not product or stale(LIB_PATH)
+    module = product and (due or stale(EXT_PATH))
+    why = ext_unavailable() if module else ""
+    if why:
+        module = False
+        if due:
+            print(f"{os.path.basename(EXT_PATH)} is not built: {why}", file=sys.stderr)
+    procs, objs = [], []
+    if due:
+        build_dir = os.path.join(ROOT, "_build", "-".join(defines) or "default")
+        os.makedirs(build_dir, exist_ok=True)
+        common = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", CSRC, "-I", INCLUDE,
+                  "--expt-relaxed-constexpr"]
+        if verbose:
+            common += ["-Xptxas", "-v"]
+        common += [f"-D{d}" for d in defines]
+        for src in SOURCES:  # translation units compile side by side
+            obj = os.path.join(build_dir, src.replace(".cu", ".o"))
+            procs.append((subprocess.Popen(common + ["-c", os.path.join(CSRC, src), "-o", obj]), src))
+            objs.append(obj)
+    ext = subprocess.Popen(ext_command(EXT_PATH + ".tmp")) if module else None
     failed = [src for proc, src in procs if proc.wait() != 0]
+    if due and not failed:
+        tmp = out_path + ".tmp"
+        subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], check=True)
+        os.replace(tmp, out_path)
+    if ext is not None:
+        if ext.wait() == 0:
+            os.replace(EXT_PATH + ".tmp", EXT_PATH)
+        else:
+            failed.append(os.path.basename(EXT_SOURCE))
     if failed:
         raise RuntimeError(f"the compiler failed on {', '.join(failed)}")
-    if product:
-        os.replace(EXT_PATH + ".tmp", EXT_PATH)
-    tmp = out_path + ".tmp"
-    subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], check=True)
-    os.replace(tmp, out_path)
     return out_path
 
 
