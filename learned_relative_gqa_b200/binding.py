@@ -493,10 +493,14 @@ def _serving():
     if _bound is None or _bound is not _lib:
         lib = load()
         try:
-            from . import _serving as ext
+            from . import _serving as ext, build
         except ImportError as e:
             raise RuntimeError("_serving.so is not built for this interpreter and PyTorch; "
                                "run python -m learned_relative_gqa_b200.build") from e
+        built_for = getattr(ext, "built_for", "an earlier version of this package")
+        if built_for != build.ext_target():
+            raise RuntimeError(f"_serving.so is built for {built_for}, this is {build.ext_target()}; "
+                               "run python -m learned_relative_gqa_b200.build")
         ext.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.inkling_kv_plan, lib.inkling_kv_append, lib.inkling_rel_attn_decode,
             lib.inkling_rel_attn_decode_workspace_size)))

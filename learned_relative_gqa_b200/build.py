@@ -51,6 +51,22 @@ def ext_unavailable() -> str:
     return "" if shutil.which("g++") else "there is no g++"
 
 
+def ext_target() -> str:
+    """What the Python module is built for: this interpreter and this PyTorch."""
+    import sysconfig
+
+    import torch
+    return f"{sysconfig.get_config_var('SOABI')}, torch {torch.__version__}"
+
+
+def ext_stale() -> bool:
+    """True when the Python module is missing, older than a source, or built for another interpreter or PyTorch."""
+    if stale(EXT_PATH):
+        return True
+    with open(EXT_PATH, "rb") as f:
+        return f"serving module for {ext_target()}\0".encode() not in f.read()
+
+
 def ext_command(out_path: str) -> list:
     """The host compiler's command line for the Python module."""
     import sysconfig
@@ -62,7 +78,8 @@ def ext_command(out_path: str) -> list:
     include = [INCLUDE, sysconfig.get_paths()["include"], cuda]
     torch_include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include")]
     return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", EXT_SOURCE, "-o", out_path]
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             f'-DINKLING_BUILT_FOR="{ext_target()}"', EXT_SOURCE, "-o", out_path]
             + [f"-I{d}" for d in include] + [a for d in torch_include for a in ("-isystem", d)]
             + [f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
 
@@ -75,12 +92,10 @@ def build(force: bool = False, verbose: bool = False, out_path: str = LIB_PATH, 
     calls of ``binding`` then say that the module is missing."""
     product = out_path == LIB_PATH and not defines
     due = force or not product or stale(LIB_PATH)
-    module = product and (due or stale(EXT_PATH))
-    why = ext_unavailable() if module else ""
-    if why:
-        module = False
-        if due:
-            print(f"{os.path.basename(EXT_PATH)} is not built: {why}", file=sys.stderr)
+    why = ext_unavailable() if product else ""
+    if why and due:
+        print(f"{os.path.basename(EXT_PATH)} is not built: {why}", file=sys.stderr)
+    module = product and not why and (due or ext_stale())
     procs, objs = [], []
     if due:
         build_dir = os.path.join(ROOT, "_build", "-".join(defines) or "default")

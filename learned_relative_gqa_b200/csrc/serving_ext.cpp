@@ -310,8 +310,18 @@ PyMethodDef method(const char* name) {
 PyMethodDef g_methods[] = {method<kv_plan>("kv_plan"), method<kv_append>("kv_append"),
                            method<paged_decode>("paged_decode"), method<bind>("bind"),
                            {nullptr, nullptr, 0, nullptr}};
+// What this file was compiled for; the build looks for it in the module, the binding in built_for.
+constexpr char kBuiltFor[] = "serving module for " INKLING_BUILT_FOR;
+
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject* PyInit__serving() { return PyModule_Create(&g_module); }
+extern "C" __attribute__((visibility("default"))) PyObject* PyInit__serving() {
+    PyObject* const m = PyModule_Create(&g_module);
+    if (m && PyModule_AddStringConstant(m, "built_for", kBuiltFor + sizeof("serving module for ") - 1) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

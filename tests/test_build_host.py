@@ -54,3 +54,30 @@ def test_a_source_that_does_not_compile_is_named(tree, capfd):
     with pytest.raises(RuntimeError, match="one.cu"):
         B.build(out_path=B.LIB_PATH)
     assert not os.path.exists(B.LIB_PATH)
+
+
+def test_module_is_due_again_for_another_pytorch(tree, monkeypatch, capfd):
+    """A module built against another PyTorch or interpreter is built again, and the library is not."""
+    import torch
+    with open(B.EXT_SOURCE, "w") as f:
+        f.write('extern "C" const char* const built_for;\nconst char* const built_for = "serving module for " INKLING_BUILT_FOR;\n')
+    B.build(out_path=B.LIB_PATH)
+    lib, ext = os.path.getmtime(B.LIB_PATH), os.path.getmtime(B.EXT_PATH)
+    B.build(out_path=B.LIB_PATH)
+    assert os.path.getmtime(B.EXT_PATH) == ext
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    assert B.ext_stale()
+    B.build(out_path=B.LIB_PATH)
+    assert not B.ext_stale()
+    assert os.path.getmtime(B.EXT_PATH) > ext and os.path.getmtime(B.LIB_PATH) == lib
+
+
+def test_module_of_another_pytorch_is_not_used(monkeypatch):
+    """The calls say so, rather than run against tensors of another layout."""
+    from learned_relative_gqa_b200 import binding
+    B.build()
+    binding._serving()
+    monkeypatch.setattr(binding, "_bound", None)
+    monkeypatch.setattr(binding._ext, "built_for", "another", raising=True)
+    with pytest.raises(RuntimeError, match="another"):
+        binding._serving()
