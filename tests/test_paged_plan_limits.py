@@ -125,3 +125,23 @@ def test_plans_of_different_sizes_from_two_threads():
     for t in threads:
         t.join()
     assert not fails, fails
+
+
+def test_plan_with_few_requests_that_give_back_many_pages():
+    """Far more pages move than there are requests and tokens: eight requests of 32768 pages end, one that
+    grows takes some of those, and the free list was not empty."""
+    from learned_relative_gqa_b200 import binding
+    N, M, page = 9, 32768, 1
+    rng = np.random.default_rng(7)
+    old, new = [M] * 8 + [5], [0, M // 2] * 4 + [1005]
+    num_pages = 8 * M + 100
+    order = rng.permutation(num_pages)
+    table = np.full((N, M), -1)
+    table[:8], table[8, :5] = order[:8 * M].reshape(8, M), order[8 * M:8 * M + 5]
+    free = np.full(num_pages, -1)
+    free[:60] = order[8 * M + 5:8 * M + 65]
+    want = ref.plan(old, new, table, free, 60, page, 1003, num_pages)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x = dict(old_lens=torch.tensor(old, **i32), new_lens=torch.tensor(new, **i32), block_table=torch.tensor(table, **i32),
+             free_pages=torch.tensor(free, **i32), free_count=torch.tensor([60], **i32))
+    same(binding.kv_plan(**x, page_size=page, num_pages=num_pages, max_tokens=1003), x, want)
