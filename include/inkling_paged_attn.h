@@ -83,7 +83,9 @@ typedef struct {
  * the requests. A request that gets fewer pages than it wants keeps as many tokens
  * as fit in the pages it has (lens), and the slots of its other new tokens are -1.
  * slots and positions behind the last new token are set to -1 and 0; new tokens
- * beyond T have no entry. Table entries other than the new pages, and entries of
+ * beyond T have no entry, though lens counts them (info[1] is how many there are,
+ * so T has to be that at least for every token to get its slot). A page belongs to
+ * one request: one that stood in two rows would be given back twice. Table entries other than the new pages, and entries of
  * free_pages at or above the new count, stay as they were. Lengths outside
  * [0, M * P] and a count outside [0, num_pages] are taken as the nearest bound; the
  * slots of tokens whose page number is outside the pool are -1. What is written
@@ -99,7 +101,8 @@ inkling_status inkling_kv_plan(const inkling_kv_plan_dims* dims, const int32_t* 
 /*
  * Appends T rows to the cache: k_cache[slots[t]] = k[t], v_cache[slots[t]] = v[t].
  * Rows whose slot is outside [0, num_pages * page_size) are skipped. Slots that are
- * stored must differ from each other, and the pools may not overlap.
+ * stored must differ from each other, and the pools may not overlap, nor a stored
+ * slot a row of k or v.
  *   tokens       T
  *   k_row, v_row elements from one token's [Hkv, D] rows to the next one's, multiples
  *                of 8 and at least Hkv * D (the rows of a fused projection)
@@ -132,7 +135,10 @@ inkling_status inkling_kv_append(const inkling_kv_cache_desc* cache, const inkli
  *   out[n,h,:] = sum_allowed exp(z_j - lse) * V[j,g,:]
  * Token j is on page block_table[n, j / page_size]; entries whose tokens are all
  * outside the window or behind lens[n] are not read. Cached values that no allowed
- * key has (the rest of the last page) may be anything, NaN and infinities included.
+ * key has (the rest of the last page) may be anything, NaN and infinities included;
+ * a value of an allowed key that is not finite makes NaN of its column. Logits are held
+ * in units of log 2: profile entries beyond 2.35e38 (BF16's lowest value, as a mask) count
+ * as infinite, and where that leaves a row no key, it is one with no allowed key.
  * A request with no allowed key (lens[n] <= 0: a padding row) gets out = 0, lse =
  * sink. A length above max_pages * page_size is taken as that.
  *   requests N, heads_q Hq (a multiple of heads_kv, below 65536), rel_extent R (a

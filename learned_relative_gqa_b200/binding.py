@@ -584,7 +584,9 @@ def kv_plan(old_lens, new_lens, block_table, free_pages, free_count, *, page_siz
     ``slots`` [max_tokens] int64, ``positions`` [max_tokens] and ``info`` [4] (pages free
     afterwards, new tokens, pages short, pages taken). ``info[:1]`` is the next call's
     ``free_count`` (see include/inkling_paged_attn.h). ``lens`` and ``info`` may be given,
-    to be written; they may not overlap an input or each other.
+    to be written; they may not overlap an input or each other. ``lens`` counts new tokens
+    beyond ``max_tokens`` too, which have no slot: ``info[1]`` tells how many tokens are new.
+    What a call allocates shares one storage (a tensor of it that is kept or saved keeps all).
     """
     if stream is not None:
         with _current(stream, block_table.device):
@@ -618,7 +620,7 @@ def paged_decode(q, k_cache, v_cache, block_table, lens, profiles=None, sink=Non
     ``k_scale``, ``v_scale`` [Hkv]), ``block_table`` [N,M] int32, ``lens`` [N] int32 with the
     new token counted (0: a padding row), ``profiles`` [N,Hq,R] BF16, ``sink`` [N,Hq] fp32
     (see include/inkling_paged_attn.h). ``workspace``: ``alloc_decode_workspace``'s, for a
-    caller that keeps one.
+    caller that keeps one. ``out`` and ``lse`` share one storage.
     """
     if stream is not None:
         with _current(stream, k_cache.device):

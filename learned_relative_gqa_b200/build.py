@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libinkling_rel_attn.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-# the same kernels with every shared / global index checked (-DINKLING_BOUNDS_CHECK), for tests
+# the same library, with every shared / global index of the attention's forward and backward kernels
+# checked (-DINKLING_BOUNDS_CHECK), for tests; the serving kernels hold no such checks
 BOUNDS_CHECK_LIB_PATH = os.path.join(HERE, "libinkling_rel_attn_boundscheck.so")
 # the serving calls on PyTorch tensors; it takes the library's entry points when that is loaded
 EXT_SOURCE = os.path.join(CSRC, "serving_ext.cpp")

@@ -65,7 +65,9 @@ class PagedKVCache:
         ``positions`` [max_tokens] and ``query_start`` [max_requests + 1] of the new tokens.
 
         ``cache.lens`` holds the lengths that the free pages allowed and ``cache.info`` the
-        pages left, the new tokens, the pages that were missing and the pages taken.
+        pages left, the new tokens, the pages that were missing and the pages taken. With
+        more new tokens than ``max_tokens`` the last ones get no slot, though ``cache.lens``
+        counts them: what ``decode`` reads for those is whatever their pages held before.
         """
         plan = binding.kv_plan(self.lens, new_lens, self.block_table, self.free_pages, self._free_count,
                                page_size=self.page_size, num_pages=self.num_pages, max_tokens=max_tokens,

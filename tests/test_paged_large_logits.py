@@ -48,3 +48,27 @@ def test_decode_of_large_logits_stays_finite(dtype, split, hq):
     assert (out - 1.5).abs().max() <= 1.5 * 2.0 ** -16
     # the sum's logarithm, and steps of the product b log2 e, of the sum and of the way back
     assert ((lse - b).abs() <= math.log(L) + 8 * math.log(2.0) + 16 * U * b.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e4m3fn, torch.bfloat16])
+@pytest.mark.parametrize("split", [False, True])
+def test_profile_rows_of_the_lowest_value_leave_no_key(dtype, split):
+    """BF16's lowest value is beyond what logits in units of log 2 hold: a row of it is a row without keys."""
+    from learned_relative_gqa_b200 import binding
+    g = torch.Generator("cuda").manual_seed(1)
+    N, hq, L, D, page = 2, 4, 300, 128, 16
+    kc, vc = (torch.randn(2 * 19, page, 1, D, generator=g, device="cuda").to(dtype) for _ in range(2))
+    table = torch.full((N, 19 + (1000 if split else 0)), -1, dtype=torch.int32, device="cuda")
+    table[:, :19] = torch.arange(38, device="cuda").view(2, 19)
+    q = torch.randn(N, hq, D, generator=g, device="cuda").to(torch.bfloat16)
+    prof = torch.zeros(N, hq, 304, dtype=torch.bfloat16, device="cuda")
+    prof[0, 1], prof[1, 3] = torch.finfo(torch.bfloat16).min, -math.inf
+    one = torch.ones(1, device="cuda")
+    scales = dict(k_scale=one, v_scale=one) if dtype == torch.float8_e4m3fn else {}
+    lens = torch.tensor([L, L - 7], dtype=torch.int32, device="cuda")
+    for sink in (None, torch.randn(N, hq, generator=g, device="cuda"), torch.full((N, hq), torch.finfo(torch.float32).min, device="cuda")):
+        out, lse = binding.paged_decode(q, kc, vc, table, lens, prof, sink, **scales)
+        for n, h in ((0, 1), (1, 3)):
+            assert not out[n, h].any()
+            assert lse[n, h] == (-math.inf if sink is None else sink[n, h])
+        assert torch.isfinite(out).all() and out[0, 0].any() and out[1, 1].any()
