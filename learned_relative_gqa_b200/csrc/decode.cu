@@ -39,12 +39,13 @@
 // the largest, whose error (2^-25 of it) is under the FP32 sum's own.
 //
 // Measured (GPU time of a call, of the measured copy bandwidth): eight requests of 32767
-// tokens, 32 / 8 heads of 128, profiles of 4096: 177 us, 6.06 TB/s, 0.93; one of 32768: 30.9
-// us, 4.35 TB/s, 0.66 (of it 5 us until the first tile is in and 4 us for the join); 64
-// requests of 16 to 4096 tokens: 41.9 us, 4.72 TB/s, 0.72; 24 requests of 8191 to 32768
-// tokens in e4m3, 32 / 4 heads: 87.1 us, 5.29 TB/s, 0.81 (a tile's dependent instructions
+// tokens, 32 / 8 heads of 128, profiles of 4096: 176 us, 6.12 TB/s, 0.93; one of 32768: 30.7
+// us, 4.38 TB/s, 0.67 (of it 5 us until the first tile is in and 4 us for the join); 64
+// requests of 16 to 4096 tokens: 41.3 us, 4.79 TB/s, 0.73; 24 requests of 8191 to 32768
+// tokens in e4m3, 32 / 4 heads: 87.2 us, 5.28 TB/s, 0.81 (a tile's dependent instructions
 // take about 2,600 cycles for its 8 KB with two warps to a scheduler, which is what HBM
-// takes as well). A plain sum over as many bytes takes 181, 29.0, 38.3 and 89.4 us.
+// takes as well; 94.5 us on some boards, in a graph or not). A plain sum over as many bytes
+// takes 181, 29.0, 38.3 and 89.4 us.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -67,11 +68,18 @@ constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 320;
 constexpr int kMaxWorkers = kMaxCtas * kWarps;  // workspace slots: two per worker
 // One CTA per unit, with no split, up to these sizes: tiles of each of its warps, and units
-// of the call. Both sides, GPU us whole / split, with 16 / 4 heads of 128 and requests of 1 to
-// 2048 tokens: window 512, 64 requests (4 warps, 8 tiles each) 12.2 / 14.1, 16 requests (8
-// warps, 4 tiles) 8.1 / 11.9; window 1024 (8 warps, 8 tiles) 1 request 11.2 / 9.4, 16
-// requests 11.2 / 11.8, 32 requests 13.0 / 12.6; window 512, 512 units 17.4 / 17.3, 800 units
-// 23.7 / 21.3.
+// of the call. Both sides, GPU us whole (its warps) and split, with 16 / 4 heads of 128 (4 units
+// to a request) and requests of 1 to 2048 tokens, W the window:
+//   requests  BF16, W 512     BF16, W 1024    e4m3, W 512     e4m3, W 1024
+//     1       6.9 (8) 10.7    10.7 (8)  9.5    5.7 (8) 10.0    8.7 (8) 11.6
+//     4       7.2 (8) 10.9    10.9 (8) 10.9    5.9 (8)  9.8    8.9 (8) 11.5
+//    16       7.6 (8) 11.9    10.8 (8) 11.6    6.1 (8) 10.6    8.8 (8) 11.9
+//    32       7.8 (8) 12.2    12.3 (8) 12.3    6.1 (8) 11.9    9.0 (8) 12.4
+//    64      11.8 (4) 13.9    15.8 (8) 15.3    8.9 (4) 11.4   13.6 (4) 12.9
+//   128      17.2 (4) 17.7    22.4 (8) 20.1   12.6 (4) 13.6   17.6 (4) 15.6
+//   200      23.3 (4) 21.0    34.4 (8) 24.5   18.5 (4) 17.2   24.7 (4) 20.1
+// So the rule is right but for two corners, where the split would be 1.2 us (a lone request with
+// 33 to 64 tiles of 16 keys) and 0.7 to 2 us (129 to 512 units of 17 to 32 tiles of 32) faster.
 constexpr int kWholeTiles = 8;
 constexpr int kWholeUnits = 512;
 constexpr int kJoinThreads = 256;

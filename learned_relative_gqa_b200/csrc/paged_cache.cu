@@ -62,8 +62,11 @@ __device__ __forceinline__ int last_at_or_below(const int* at, int n, int x) {
 // items. The stack needs no order between blocks either: a page popped in the same call that
 // returned it is read from the block table, so no block reads an entry of free_pages or of
 // the table that another one writes. The code is kept short: it is as cold as the data.
-// GPU time: 64 requests of one token each 3.0 us, 256 prompts (239,480 tokens) 5.2 us, 4096
-// requests (117,153 tokens) 8.6 us.
+// GPU time: 64 requests of one token each 3.1 us, 256 prompts (239,480 tokens) 5.3 us, 4096
+// requests (117,153 tokens) 8.5 us, 8192 (233,359) 19.8 us, 16384 (464,073) 59.6 us: from 4096
+// requests on the sums' shared-memory bank conflicts count (a thread's requests stand next to
+// each other, so its neighbours are 4, 8 or 16 words away: 429,352 conflicts at 4096, 3,460
+// cycles of each block).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanParams p) {
     extern __shared__ int s_at[];
     int* s_tok = s_at;               // [N + 1] exclusive prefix sums, totals at [N]
@@ -288,12 +291,15 @@ constexpr int kPerLane = E4M3 ? 16 : 8;
 
 // One (token, head) row of k and of v per group of lanes, 16-byte loads and one 16-byte store
 // of each to a lane, all rows of a token next to each other. A stream of 4 (BF16) or 3
-// (e4m3) bytes per value, bound by HBM; e4m3 by its arithmetic too (77 % of the issue slots
-// with 8 values to a lane, which is why a lane has 16). No loop, so that a full SM keeps
-// 2048 threads' loads in flight. The clip's sum of squares is FP32 over the group by shuffles.
-// 32768 clipped rows of 8 x 128: 41.8 us, 6.43 TB/s; 16381 clipped rows of 4 x 128 to e4m3
-// 11.4 us, 4.4 TB/s; one step of 64 rows: 1.3 us. (128 threads to a block: with 256, 11.6 and
-// 1.5 us; held to fewer registers, the e4m3 form spills and takes 12.9 us and more.)
+// (e4m3) bytes per value, bound by HBM; the clipped e4m3 form by how many threads an SM holds
+// and by its arithmetic between loads and stores (61 % of the issue slots busy; 77 % with 8
+// values to a lane, which is why a lane has 16). No loop, so that a full SM keeps the loads of
+// all its threads in flight: 2048 in BF16 (18 and 32 registers), 1536 and, clipped, 1280 in
+// e4m3 (40 and 48). The clip's sum of squares is FP32 over the group by shuffles.
+// 32768 clipped rows of 8 x 128: 42.1 us, 6.39 TB/s; 16381 clipped rows of 4 x 128 to e4m3
+// 11.4 us, 4.4 TB/s, unclipped 8.4 us, 6.0 TB/s; one step of 64 rows: 1.3 us. (128 threads to a
+// block: with 256, 11.6 and 1.5 us; held to fewer registers, the clipped e4m3 form spills and
+// takes 12.9 us and more.)
 template <int D, bool E4M3, bool CLIP>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int PER = kPerLane<E4M3>, LPR = D / PER;
@@ -449,9 +455,9 @@ inkling_status inkling_kv_plan(const inkling_kv_plan_dims* dims, const int32_t* 
                                                    int((kPlanMaxRequests + 1) * 12));
         if (e != cudaSuccess) return status_of(e);
     }
-    // At most one block per SM: more would only repeat the prefix sums. The pages taken and
-    // returned are not known here; they are fewer than the tokens and requests, or many
-    // rounds of the loop in any case.
+    // At most one block per SM of a B200: more would only repeat the prefix sums. The pages taken
+    // and returned are not known here and not counted: few requests that give back very many are
+    // rounds of the loop on few blocks (16,384 pages of 8 requests 12 us, 262,144 of 8 143 us).
     const size_t want = (T + 2 * N + 1 + kPlanThreads - 1) / kPlanThreads;
     return status_of(launch_early(plan_kernel, dim3(unsigned(want < 148 ? want : 148)), kPlanThreads, smem,
                                   static_cast<cudaStream_t>(stream), p));
