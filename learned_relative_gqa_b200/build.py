@@ -112,15 +112,17 @@ def build(force: bool = False, verbose: bool = False, out_path: str = LIB_PATH, 
             objs.append(obj)
     ext = subprocess.Popen(ext_command(EXT_PATH + ".tmp")) if module else None
     failed = [src for proc, src in procs if proc.wait() != 0]
+    built = ext is not None and ext.wait() == 0
     if due and not failed:
         tmp = out_path + ".tmp"
         subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], check=True)
+        if product and not built and os.path.exists(EXT_PATH):
+            os.remove(EXT_PATH)  # an older module may not fit the new library
         os.replace(tmp, out_path)
-    if ext is not None:
-        if ext.wait() == 0:
-            os.replace(EXT_PATH + ".tmp", EXT_PATH)
-        else:
-            failed.append(os.path.basename(EXT_SOURCE))
+    if built and not failed:  # nor a new one an older library
+        os.replace(EXT_PATH + ".tmp", EXT_PATH)
+    if ext is not None and not built:
+        failed.append(os.path.basename(EXT_SOURCE))
     if failed:
         raise RuntimeError(f"the compiler failed on {', '.join(failed)}")
     return out_path

@@ -44,8 +44,8 @@
 // requests of 16 to 4096 tokens: 41.3 us, 4.79 TB/s, 0.73; 24 requests of 8191 to 32768
 // tokens in e4m3, 32 / 4 heads: 87.2 us, 5.28 TB/s, 0.81 (a tile's dependent instructions
 // take about 2,600 cycles for its 8 KB with two warps to a scheduler, which is what HBM
-// takes as well; 94.5 us on some boards, in a graph or not). A plain sum over as many bytes
-// takes 181, 29.0, 38.3 and 89.4 us.
+// takes as well; calls of 92 to 95 us were seen on other boards). A plain sum over as many
+// bytes takes 181, 29.0, 38.3 and 89.4 us.
 #include <algorithm>
 #include <atomic>
 #include <cmath>

@@ -43,6 +43,9 @@ def test_library_is_built_without_a_host_compiler_for_the_module(tree, monkeypat
 def test_a_module_that_does_not_compile_leaves_the_library_built(tree, capfd):
     with open(B.EXT_SOURCE, "w") as f:
         f.write("this is no source\n")
+    with open(B.EXT_PATH, "w") as f:
+        f.write("an older module, which may not fit the new library")
+    os.utime(B.EXT_PATH, (0, 0))
     with pytest.raises(RuntimeError, match="serving_ext.cpp"):
         B.build(out_path=B.LIB_PATH)
     assert os.path.exists(B.LIB_PATH) and not os.path.exists(B.EXT_PATH)
@@ -53,7 +56,7 @@ def test_a_source_that_does_not_compile_is_named(tree, capfd):
         f.write("this is no source\n")
     with pytest.raises(RuntimeError, match="one.cu"):
         B.build(out_path=B.LIB_PATH)
-    assert not os.path.exists(B.LIB_PATH)
+    assert not os.path.exists(B.LIB_PATH) and not os.path.exists(B.EXT_PATH)
 
 
 def test_module_is_due_again_for_another_pytorch(tree, monkeypatch, capfd):
